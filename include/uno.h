@@ -55,6 +55,8 @@ typedef enum { UNO_BF16 = 0, UNO_F32 = 1 } uno_dtype;
 #define UNO_DEV_BAD_DRAFT 1 /* a draft id outside [0, V): that sequence's outputs are -1 */
 #define UNO_DEV_NAN 2       /* a NaN logit in a row that was read: outputs are -1 */
 #define UNO_DEV_TIMEOUT 4   /* a bounded on-device wait gave up (kernel returned early) */
+#define UNO_DEV_BAD_INDEX 8 /* a token id or a slot outside its range: that entry was skipped */
+#define UNO_DEV_NO_TOKEN 16 /* a logits row whose mask allows no token: its logits are all -inf */
 
 /* Message for the last failed call on this thread (static storage, valid
  * until the next call on this thread). Never NULL. */
@@ -144,6 +146,61 @@ uno_status uno_gated_lora_linear_group(uno_dtype dt, int64_t M, int64_t K, int32
                                        const uint8_t* gate, float scale, int32_t mode,
                                        void* const* y, void* workspace, size_t ws_bytes,
                                        void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit weights: e4m3 codes with one float scale per block of 128 (a library
+ * addition; the pages' weights are bf16). A frozen theta_AR held this way takes
+ * half the memory and half the HBM traffic of a decode step; the adapter
+ * theta_Delta stays bf16 and trains over it.
+ *
+ * uno_fp8_quantize: x [M,K] `dt` (bf16 or f32) in blocks of block_rows x 128
+ *   (block_rows 1: activations, 128: weights; ragged at the edges):
+ *     a = max(max_block |x|, 2^-100), scale = a / 448,
+ *     code = e4m3(x * (448 / a)), nearest even, in float until the code.
+ *   codes [M,K] e4m3 bytes; scales [ceil(M/block_rows), ceil(K/128)] float.
+ *   K a multiple of 8. A block with a NaN gets NaN scale and codes, one with an
+ *   infinity an infinite scale. An all-zero block has codes 0.
+ *
+ * uno_gated_lora_linear_fp8: the gated-LoRA linear with W in 128 x 128 blocks,
+ *     y = x^ W^^T + scale * g (.) ((x A^T) Bl^T)
+ *   W^ = Wq * Ws blockwise, Wq [N,K] e4m3 bytes, Ws [ceil(N/128),
+ *   ceil(K/128)] float; x^ = x [M,K] bf16 quantised in 1 x 128 blocks as
+ *   uno_fp8_quantize does; y [M,N] bf16. Each block of 128 k is summed in fp32
+ *   on the tensor core and scaled in fp32. The adapter reads x itself: A [r,K]
+ *   and Bl [N,r] bf16, x A^T rounded to bf16 as in uno_gated_lora_linear.
+ *   dt must be UNO_BF16. Sizes: M >= 0 (0 launches nothing), K a multiple of
+ *   16, N and r of 8, 0 <= r <= 256, M and K <= 2^24, N <= 2^23.
+ *
+ * uno_gated_lora_input_grad_fp8: its gradient with respect to x for an output
+ *   gradient dy [M,N] bf16 (the rounding of x and dy to 8 bits is taken as the
+ *   identity):
+ *     dx = dy^ W^ + scale * g (.) ((dy Bl) A)          [M,K] bf16
+ *   dy^ = dy in 1 x 128 blocks along N; the weight comes transposed, laid out
+ *   once by the caller: Wqt [K,N] e4m3 bytes, Wst [ceil(K/128), ceil(N/128)].
+ *   A [r,K] and Bl [N,r] as in the forward pass. N a multiple of 16, K and r of
+ *   8, M and N <= 2^24, K <= 2^23. The adapter's own gradients do not depend on
+ *   W: uno_gated_lora_backward.
+ *
+ *   Every pointer 16-byte aligned; workspace >= the matching query (also for
+ *   r = 0), any contents; calls that share one must not run at the same time.
+ * ------------------------------------------------------------------------- */
+uno_status uno_fp8_quantize(uno_dtype dt, int64_t M, int64_t K, int32_t block_rows, const void* x,
+                            void* codes, float* scales, void* stream);
+
+size_t uno_gated_lora_linear_fp8_workspace(int64_t M, int64_t K, int64_t N, int32_t r);
+
+uno_status uno_gated_lora_linear_fp8(uno_dtype dt, int64_t M, int64_t K, int64_t N, int32_t r,
+                                     const void* x, const void* Wq, const float* Ws, const void* A,
+                                     const void* Bl, const uint8_t* gate, float scale, void* y,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
+size_t uno_gated_lora_input_grad_fp8_workspace(int64_t M, int64_t K, int64_t N, int32_t r);
+
+uno_status uno_gated_lora_input_grad_fp8(uno_dtype dt, int64_t M, int64_t K, int64_t N, int32_t r,
+                                         const void* dy, const void* Wqt, const float* Wst,
+                                         const void* A, const void* Bl, const uint8_t* gate,
+                                         float scale, void* dx, void* workspace, size_t ws_bytes,
+                                         void* stream);
 
 /* ---------------------------------------------------------------------------
  * Psi-Spec verification of one drafted block per sequence (hyper.ai page,
@@ -344,6 +401,57 @@ uno_status uno_draft_sample(uno_dtype dt, int32_t B, int32_t k, int32_t V, const
                             float temperature, uint64_t seed, uint64_t step, uint64_t seq_offset,
                             int32_t* draft, int32_t* dev_status, void* workspace,
                             size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rules on logits, applied before drafting, verification or distillation (a
+ * library addition: sampling from a distribution the user has penalised,
+ * biased or masked stays lossless with respect to that distribution when the
+ * AR rows get the rules of their own prefixes).
+ *
+ * Token records: counts [S,V] 16-bit words, one row (slot) per sequence. Bit 15:
+ *   the id occurs in the prompt; bits 0..14: how often it was emitted
+ *   (saturating at 32767). A new sequence's row is zeroed by the caller.
+ *
+ * uno_token_counts_add: for each sequence b the ids tokens[b, 0 .. lens[b])
+ *   (lens NULL: all T; a length past T counts as T) set bit 15 (prompt = 1) or
+ *   add one each (prompt = 0) in row slots[b] (slots NULL: row b, S >= B).
+ *   tokens [B,T] int32; -1 is skipped (the padding of out_tokens), so a
+ *   verified block is added as it comes. Any other id outside [0, V) or a
+ *   slot outside [0, S) is skipped and sets UNO_DEV_BAD_INDEX.
+ *
+ * uno_logits_process: out [B,R,V] from logits [B,R,V] `dt`, row j of sequence b:
+ *     n(v)  = emitted count of v in row slots[b] of counts (0 without counts)
+ *             + occurrences of v among the row's path tokens
+ *     z' = z > 0 ? z / repetition[b] : z * repetition[b]   where n(v) > 0 or v is
+ *          in the prompt
+ *     z' = z' - frequency[b] n(v) - presence[b] [n(v) > 0]
+ *     z' = z' + sum of bias[b,i] over bias_ids[b,i] = v
+ *     z' = -inf   where bit v of mask[b,j] is 0 (whatever the logit was)
+ *   in float, rounded once to `dt`. Path tokens: path [B,P] (path_per_row 0) is
+ *   the drafted block, of which row j follows the first min(j, P) ids (the k or
+ *   k + 1 AR rows of uno_psi_verify); path [B,R,P] (path_per_row 1) gives each
+ *   row its own ids (the nodes of uno_tree_verify). -1 entries of path and
+ *   bias_ids are skipped, other ids outside [0, V) too with UNO_DEV_BAD_INDEX.
+ *   A slot outside [0, S) counts as an empty record and sets that bit.
+ *   repetition (> 0), frequency, presence [B] float, NULL: 1, 0, 0. bias_ids
+ *   [B,nb] int32, bias [B,nb] float (nb = 0: none). mask [B,R,ceil(V/32)]
+ *   words, bit v % 32 of word v / 32, NULL: all allowed. A row that allows
+ *   nothing gets -inf everywhere and sets UNO_DEV_NO_TOKEN.
+ *   out may be logits itself; it must not overlap it otherwise. 2 <= V <=
+ *   196608, P <= 64, nb <= 1024; B = 0 or R = 0 launches nothing. logits, out,
+ *   counts and mask 16-byte aligned. No workspace.
+ * ------------------------------------------------------------------------- */
+uno_status uno_token_counts_add(int32_t S, int32_t V, uint16_t* counts, int32_t B, int32_t T,
+                                const int32_t* tokens, const int32_t* lens, const int32_t* slots,
+                                int32_t prompt, int32_t* dev_status, void* stream);
+
+uno_status uno_logits_process(uno_dtype dt, int32_t B, int32_t R, int32_t V, const void* logits,
+                              void* out, int32_t S, const uint16_t* counts, const int32_t* slots,
+                              int32_t P, int32_t path_per_row, const int32_t* path,
+                              const float* repetition, const float* frequency,
+                              const float* presence, int32_t nb, const int32_t* bias_ids,
+                              const float* bias, const uint32_t* mask, int32_t* dev_status,
+                              void* stream);
 
 /* ---------------------------------------------------------------------------
  * Philox uniforms, exposed so the generator can be checked bit for bit:

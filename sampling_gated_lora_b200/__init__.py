@@ -8,6 +8,13 @@ Functions mirror the C ABI:
     gated_lora_linear  y = x W^T + s g (x A^T) Bl^T
     psi_verify         accept u q(d) < p(d), longest prefix, residual / bonus draw
     draft_sample       linear-sampler draft from softmax(q / T)
+    gated_lora_adapter_grads  dA, dBl of the adapter, W frozen
+    fp8_quantize       e4m3 codes and a float scale per block of 128
+    gated_lora_linear_fp8, gated_lora_input_grad_fp8
+                       the gated linear over 8-bit weights, and its input gradient
+    token_counts_add, logits_process
+                       token records; repetition, frequency and presence penalties,
+                       biases and grammar masks on logits
     philox_uniforms    the generator's words and uniforms, for bit-exact checks
     rmsnorm, silu_mul  the step's glue operations
     Model              synthetic decoder stack + LM head; Model.step = uno_psi_step
@@ -21,7 +28,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libuno.so")
 
 UNO_BF16, UNO_F32 = 0, 1
-DEV_BAD_DRAFT, DEV_NAN, DEV_TIMEOUT = 1, 2, 4
+DEV_BAD_DRAFT, DEV_NAN, DEV_TIMEOUT, DEV_BAD_INDEX, DEV_NO_TOKEN = 1, 2, 4, 8, 16
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT",
                 5: "DEVICE_FLAG", 6: "WORKSPACE"}
 
@@ -30,9 +37,13 @@ EXPORTS = [
     "uno_gated_lora_linear_workspace", "uno_gated_lora_linear",
     "uno_gated_lora_linear_group_workspace", "uno_gated_lora_linear_group",
     "uno_gated_lora_backward_workspace", "uno_gated_lora_backward",
+    "uno_fp8_quantize",
+    "uno_gated_lora_linear_fp8_workspace", "uno_gated_lora_linear_fp8",
+    "uno_gated_lora_input_grad_fp8_workspace", "uno_gated_lora_input_grad_fp8",
     "uno_psi_verify_workspace", "uno_psi_verify", "uno_psi_verify_noalloc",
     "uno_draft_sample_workspace", "uno_draft_sample", "uno_distill",
     "uno_tree_verify_workspace", "uno_tree_verify",
+    "uno_token_counts_add", "uno_logits_process",
     "uno_philox_uniforms",
     "uno_model_create", "uno_model_destroy", "uno_psi_step_workspace", "uno_psi_step",
     "uno_psi_step_hidden", "uno_psi_step_kernel_count", "uno_model_profile",
@@ -77,6 +88,13 @@ def load():
         "uno_gated_lora_backward_workspace": (sz, [i64, i64, i64, i32]),
         "uno_gated_lora_backward": (i32, [i32, i64, i64, i64, i32, vp, vp, vp, vp, vp, f32, vp,
                                           vp, vp, sz, vp]),
+        "uno_fp8_quantize": (i32, [i32, i64, i64, i32, vp, vp, vp, vp]),
+        "uno_gated_lora_linear_fp8_workspace": (sz, [i64, i64, i64, i32]),
+        "uno_gated_lora_linear_fp8": (i32, [i32, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, f32,
+                                            vp, vp, sz, vp]),
+        "uno_gated_lora_input_grad_fp8_workspace": (sz, [i64, i64, i64, i32]),
+        "uno_gated_lora_input_grad_fp8": (i32, [i32, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp,
+                                                f32, vp, vp, sz, vp]),
         "uno_psi_verify_workspace": (sz, [i32, i32, i32, i32]),
         "uno_psi_verify": (i32, [i32, i32, i32, i32, i32, vp, vp, vp, f32, u64, u64, u64, vp, vp,
                                  vp, vp, vp, sz, vp]),
@@ -88,6 +106,9 @@ def load():
                                   vp, vp, vp, vp, vp, sz, vp]),
         "uno_distill": (i32, [i32, i32, i32, vp, vp, f32, f32, f32, vp, vp, vp, vp]),
         "uno_draft_sample": (i32, [i32, i32, i32, i32, vp, f32, u64, u64, u64, vp, vp, vp, sz, vp]),
+        "uno_token_counts_add": (i32, [i32, i32, vp, i32, i32, vp, vp, vp, i32, vp, vp]),
+        "uno_logits_process": (i32, [i32, i32, i32, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, vp,
+                                     vp, i32, vp, vp, vp, vp, vp]),
         "uno_philox_uniforms": (i32, [u64, u64, u32, u32, i64, vp, vp, vp]),
         "uno_model_create": (i32, [vp, i32, i32, i32, i32, i32, i32, i32, f32, vp]),
         "uno_model_destroy": (None, [vp]),
@@ -308,6 +329,97 @@ def gated_lora_adapter_grads(x, dy, A, Bl, gate, scale=1.0, dA=None, dBl=None, w
     return dA, dBl
 
 
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def fp8_quantize(x, block_rows=1, codes=None, scales=None, stream=None):
+    """(codes [M,K] float8_e4m3fn, scales [ceil(M/block_rows), ceil(K/128)] float32) of x [M,K]
+    (bf16 or f32) in blocks of block_rows (1 or 128) x 128: scale = max |x| / 448."""
+    torch = _torch()
+    _expect(x, (None, None), _floats(), "x")
+    M, K = x.shape
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    shape = (M if block_rows == 1 else _blocks(M), _blocks(K))
+    _expect(codes, (M, K), (torch.float8_e4m3fn,), "codes", optional=True)
+    _expect(scales, shape, (torch.float32,), "scales", optional=True)
+    L = load()
+    if codes is None:
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+    dev = _dev(x, codes, scales)
+    _launch(dev, stream, L.uno_fp8_quantize, _dtype(x), M, K, block_rows, _ptr(x), _ptr(codes),
+            _ptr(scales))
+    return codes, scales
+
+
+def gated_lora_linear_fp8_workspace(M, K, N, r):
+    """Bytes of the workspace of gated_lora_linear_fp8."""
+    return load().uno_gated_lora_linear_fp8_workspace(M, K, N, r)
+
+
+def gated_lora_linear_fp8(x, Wq, Ws, A, Bl, gate, scale=1.0, y=None, workspace=None, stream=None):
+    """y [M,N] = x W^T + scale * gate (x A^T) Bl^T over an 8-bit weight: Wq [N,K] float8_e4m3fn with
+    Ws [ceil(N/128), ceil(K/128)] float32 (fp8_quantize(W, 128)); x is quantised per row and block of
+    128 for the product with W, the adapter reads it as it is. bf16 x, A, Bl and y; A = Bl = None: no
+    adapter."""
+    torch = _torch()
+    bf16, f8, f32 = (torch.bfloat16,), (torch.float8_e4m3fn,), (torch.float32,)
+    _expect(x, (None, None), bf16, "x")
+    M, K = x.shape
+    _expect(Wq, (None, K), f8, "Wq")
+    N = Wq.shape[0]
+    _expect(Ws, (_blocks(N), _blocks(K)), f32, "Ws")
+    r = A.shape[0] if A is not None else 0
+    _expect(A, (r, K), bf16, "A", optional=r == 0)
+    _expect(Bl, (N, r), bf16, "Bl", optional=r == 0)
+    _expect(gate, (M,), (torch.uint8,), "gate", optional=r == 0)
+    _expect(y, (M, N), bf16, "y", optional=True)
+    L = load()
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    dev = _dev(x, Wq, Ws, A, Bl, gate, y, workspace)
+    ws, wsb = _workspace(L.uno_gated_lora_linear_fp8_workspace(M, K, N, r), dev, workspace)
+    _launch(dev, stream, L.uno_gated_lora_linear_fp8, UNO_BF16, M, K, N, r, _ptr(x), _ptr(Wq),
+            _ptr(Ws), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(y), _ptr(ws), wsb)
+    return y
+
+
+def gated_lora_input_grad_fp8_workspace(M, K, N, r):
+    """Bytes of the workspace of gated_lora_input_grad_fp8."""
+    return load().uno_gated_lora_input_grad_fp8_workspace(M, K, N, r)
+
+
+def gated_lora_input_grad_fp8(dy, Wqt, Wst, A, Bl, gate, scale=1.0, dx=None, workspace=None,
+                              stream=None):
+    """dx [M,K] = dy W + scale * gate (dy Bl) A, the input gradient of gated_lora_linear_fp8 for dy
+    [M,N] bf16. The weight comes transposed, laid out once: Wqt = Wq.t().contiguous() [K,N],
+    Wst = Ws.t().contiguous(); A [r,K] and Bl [N,r] as in the forward pass. dy is quantised per row
+    and block of 128 along N for the product with W."""
+    torch = _torch()
+    bf16, f8, f32 = (torch.bfloat16,), (torch.float8_e4m3fn,), (torch.float32,)
+    _expect(dy, (None, None), bf16, "dy")
+    M, N = dy.shape
+    _expect(Wqt, (None, N), f8, "Wqt")
+    K = Wqt.shape[0]
+    _expect(Wst, (_blocks(K), _blocks(N)), f32, "Wst")
+    r = A.shape[0] if A is not None else 0
+    _expect(A, (r, K), bf16, "A", optional=r == 0)
+    _expect(Bl, (N, r), bf16, "Bl", optional=r == 0)
+    _expect(gate, (M,), (torch.uint8,), "gate", optional=r == 0)
+    _expect(dx, (M, K), bf16, "dx", optional=True)
+    L = load()
+    if dx is None:
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
+    dev = _dev(dy, Wqt, Wst, A, Bl, gate, dx, workspace)
+    ws, wsb = _workspace(L.uno_gated_lora_input_grad_fp8_workspace(M, K, N, r), dev, workspace)
+    _launch(dev, stream, L.uno_gated_lora_input_grad_fp8, UNO_BF16, M, K, N, r, _ptr(dy), _ptr(Wqt),
+            _ptr(Wst), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(dx), _ptr(ws), wsb)
+    return dx
+
+
 def _verify_shapes(p_logits, q_logits, draft, accepted_len, out_tokens, out_count, dev_status):
     torch = _torch()
     _expect(p_logits, (None, None, None), _floats(), "p_logits")
@@ -444,6 +556,66 @@ def draft_sample(q_logits, temperature, seed, step, seq_offset=0, draft=None, de
             float(temperature), int(seed), int(step), int(seq_offset), _ptr(draft),
             _ptr(dev_status), _ptr(ws), wsb)
     return draft
+
+
+def token_counts_add(counts, tokens, lens=None, slots=None, prompt=False, dev_status=None,
+                     stream=None):
+    """Add tokens [B,T] int32 (the first lens[b] of each row; -1 skipped) to the token records counts
+    [S,V] int16, rows slots [B] (default: row b): bit 15 = in the prompt (prompt=True sets it),
+    bits 0-14 = times emitted (prompt=False adds one each). Returns counts."""
+    torch = _torch()
+    i32 = (torch.int32,)
+    _expect(counts, (None, None), (torch.int16,), "counts")
+    S, V = counts.shape
+    _expect(tokens, (None, None), i32, "tokens")
+    B, T = tokens.shape
+    _expect(lens, (B,), i32, "lens", optional=True)
+    _expect(slots, (B,), i32, "slots", optional=True)
+    _expect(dev_status, (1,), i32, "dev_status", optional=True)
+    L = load()
+    dev = _dev(counts, tokens, lens, slots, dev_status)
+    _launch(dev, stream, L.uno_token_counts_add, S, V, _ptr(counts), B, T, _ptr(tokens), _ptr(lens),
+            _ptr(slots), 1 if prompt else 0, _ptr(dev_status))
+    return counts
+
+
+def logits_process(logits, out=None, counts=None, slots=None, draft=None, repetition=None,
+                   frequency=None, presence=None, bias_ids=None, bias=None, mask=None,
+                   dev_status=None, stream=None):
+    """Rules on logits [B,R,V] (bf16 or f32) before they are sampled or verified; out may be logits.
+
+    counts [S,V] int16 token records (token_counts_add), rows slots [B] int32 (default: row b);
+    draft [B,P] int32: row j follows its first j ids, or [B,R,P]: each row's own path (-1 padded);
+    repetition, frequency, presence [B] float32; bias_ids [B,nb] int32 (-1: none) with bias [B,nb]
+    float32; mask [B,R,ceil(V/32)] int32 words, bit v % 32 of word v // 32 set: id v allowed, else -inf.
+    """
+    torch = _torch()
+    i32, f32 = (torch.int32,), (torch.float32,)
+    _expect(logits, (None, None, None), _floats(), "logits")
+    B, R, V = logits.shape
+    _expect(out, (B, R, V), (logits.dtype,), "out", optional=True)
+    _expect(counts, (None, V), (torch.int16,), "counts", optional=True)
+    _expect(slots, (B,), i32, "slots", optional=True)
+    per_row = draft is not None and draft.dim() == 3
+    _expect(draft, (B, R, None) if per_row else (B, None), i32, "draft", optional=True)
+    _expect(repetition, (B,), f32, "repetition", optional=True)
+    _expect(frequency, (B,), f32, "frequency", optional=True)
+    _expect(presence, (B,), f32, "presence", optional=True)
+    _expect(bias_ids, (B, None), i32, "bias_ids", optional=bias is None)
+    nb = 0 if bias_ids is None else bias_ids.shape[1]
+    _expect(bias, (B, nb), f32, "bias", optional=bias_ids is None)
+    _expect(mask, (B, R, (V + 31) // 32), i32, "mask", optional=True)
+    _expect(dev_status, (1,), i32, "dev_status", optional=True)
+    L = load()
+    out = torch.empty_like(logits) if out is None else out
+    dev = _dev(logits, out, counts, slots, draft, repetition, frequency, presence, bias_ids, bias,
+               mask, dev_status)
+    _launch(dev, stream, L.uno_logits_process, _dtype(logits), B, R, V, _ptr(logits), _ptr(out),
+            0 if counts is None else counts.shape[0], _ptr(counts), _ptr(slots),
+            0 if draft is None else draft.shape[-1], 1 if per_row else 0, _ptr(draft),
+            _ptr(repetition), _ptr(frequency), _ptr(presence), nb, _ptr(bias_ids), _ptr(bias),
+            _ptr(mask), _ptr(dev_status))
+    return out
 
 
 def philox_uniforms(seed, step, stream_id, index0, n, device="cuda", stream=None):

@@ -331,6 +331,162 @@ uno_status uno_gated_lora_backward(uno_dtype dt, int64_t M, int64_t K, int64_t N
   return adapter_backward_launch(M, K, N, r, x, dy, A, Bl, gate, scale, dA, dBl, workspace, st);
 }
 
+// ---------------------------------------------------------------- 8-bit linear
+
+namespace {
+
+// Workspace of an 8-bit linear call with the product's contracted size Kc and
+// output size No: the activations' codes, their scales (K-block major), t,
+// and for the input gradient the adapter transposed.
+struct Fp8Layout {
+  size_t xq, sx, t, at, blt, total;
+  int64_t ld_sx;
+};
+
+Fp8Layout fp8_layout(int64_t M, int64_t Kc, int64_t No, int32_t r, bool transposed) {
+  Fp8Layout l{};
+  l.ld_sx = (M + 127) / 128 * 128;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += align_up(bytes);
+    return o;
+  };
+  l.xq = take(static_cast<size_t>(M) * Kc);
+  l.sx = take(static_cast<size_t>((Kc + 127) / 128) * l.ld_sx * sizeof(float));
+  l.t = take(static_cast<size_t>(M) * r * 2);
+  l.at = l.blt = 0;
+  if (transposed) {
+    l.at = take(static_cast<size_t>(No) * r * 2);
+    l.blt = take(static_cast<size_t>(Kc) * r * 2);
+  }
+  l.total = off;
+  return l;
+}
+
+uno_status check_fp8(uno_dtype dt, int64_t M, int64_t Kc, int64_t No, int32_t r, const char* kc,
+                     const char* no) {
+  if (dt != UNO_BF16)
+    return set_error(UNO_ERR_UNSUPPORTED, "the 8-bit linear takes bf16 activations only");
+  if (M < 0 || Kc < 1 || No < 1 || r < 0)
+    return set_error(UNO_ERR_INVALID_ARG, "bad sizes M=%lld %s=%lld %s=%lld r=%d",
+                     static_cast<long long>(M), kc, static_cast<long long>(Kc), no,
+                     static_cast<long long>(No), r);
+  if (Kc % 16 || No % 8 || r % 8)
+    return set_error(UNO_ERR_UNSUPPORTED,
+                     "%s must be a multiple of 16, %s and r of 8 (16-byte rows): %s=%lld %s=%lld r=%d",
+                     kc, no, kc, static_cast<long long>(Kc), no, static_cast<long long>(No), r);
+  if (r > 256) return set_error(UNO_ERR_UNSUPPORTED, "rank r=%d > 256", r);
+  if (M > (1ll << 24) || Kc > (1ll << 24) || No > (1ll << 23))
+    return set_error(UNO_ERR_UNSUPPORTED, "M or %s above 2^24, or %s above 2^23", kc, no);
+  return UNO_OK;
+}
+
+// y [M,No] = x Wq^T (block scales) + scale gate (x A^T) Bl^T; `transposed`: A
+// [r, No] and Bl [Kc, r] come as the forward pass holds them and are transposed
+// here. Launches: (transposes,) quantisation, down-projection, product.
+uno_status run_fp8(int64_t M, int64_t Kc, int64_t No, int32_t r, const void* x, const void* Wq,
+                   const float* Ws, const void* A, const void* Bl, const uint8_t* gate, float scale,
+                   void* y, void* workspace, size_t ws_bytes, bool transposed, cudaStream_t st) {
+  if (!x || !Wq || !Ws || !y)
+    return set_error(UNO_ERR_INVALID_ARG, "the input, codes, scales and output must be non-NULL");
+  if (r > 0 && (!A || !Bl || !gate))
+    return set_error(UNO_ERR_INVALID_ARG, "A, Bl and gate must be non-NULL when r > 0");
+  if (!aligned16(x) || !aligned16(Wq) || !aligned16(Ws) || !aligned16(y) ||
+      (r > 0 && (!aligned16(A) || !aligned16(Bl))))
+    return set_error(UNO_ERR_INVALID_ARG, "every matrix must be 16-byte aligned");
+  const Fp8Layout L = fp8_layout(M, Kc, No, r, transposed);
+  if (!workspace || ws_bytes < L.total || !aligned16(workspace))
+    return set_error(UNO_ERR_WORKSPACE, "workspace must hold %zu bytes (got %zu)", L.total, ws_bytes);
+  char* base = static_cast<char*>(workspace);
+  uno_status s;
+  if (transposed && r > 0) {
+    // first, so that the launch that trails the quantisation (which never lets
+    // its dependents start early) may prefetch both as constants
+    if ((s = transpose2_launch(A, r, No, base + L.at, Bl, Kc, r, base + L.blt, st)) != UNO_OK) return s;
+    A = base + L.blt;
+    Bl = base + L.at;
+  }
+  float* sx = reinterpret_cast<float*>(base + L.sx);
+  if ((s = fp8_quantize_launch(UNO_BF16, M, Kc, 1, x, reinterpret_cast<uint8_t*>(base + L.xq), sx, 1,
+                               L.ld_sx, st)) != UNO_OK)
+    return s;
+  if (r > 0) {
+    const void* As[1] = {A};
+    GemmLaunch down{};
+    if ((s = gemm_prepare(down_problem(UNO_BF16, M, Kc, r, x, As, 1, gate, 0, scale, base + L.t),
+                          &down)) != UNO_OK)
+      return s;
+    if ((s = gemm_run(down, st)) != UNO_OK) return s;
+  }
+  Fp8Gemm g{};
+  g.M = M;
+  g.K = Kc;
+  g.N = No;
+  g.r = r;
+  g.xq = base + L.xq;
+  g.sx = sx;
+  g.ld_sx = L.ld_sx;
+  g.wq = Wq;
+  g.sw = Ws;
+  g.t = base + L.t;
+  g.Bl = Bl;
+  g.y = y;
+  return fp8_gemm_launch(g, st);
+}
+
+}  // namespace
+
+uno_status uno_fp8_quantize(uno_dtype dt, int64_t M, int64_t K, int32_t block_rows, const void* x,
+                            void* codes, float* scales, void* stream) {
+  if (!valid_dtype(dt)) return set_error(UNO_ERR_INVALID_ARG, "unknown dtype %d", dt);
+  if (M < 0 || K < 1)
+    return set_error(UNO_ERR_INVALID_ARG, "bad sizes M=%lld K=%lld", static_cast<long long>(M),
+                     static_cast<long long>(K));
+  if (block_rows != 1 && block_rows != 128)
+    return set_error(UNO_ERR_INVALID_ARG, "block_rows=%d must be 1 or 128", block_rows);
+  if (K % 8)
+    return set_error(UNO_ERR_UNSUPPORTED, "K=%lld must be a multiple of 8", static_cast<long long>(K));
+  if (M > (1ll << 30) || K > (1ll << 30)) return set_error(UNO_ERR_UNSUPPORTED, "sizes above 2^30");
+  if (M == 0) return UNO_OK;
+  if (!x || !codes || !scales) return set_error(UNO_ERR_INVALID_ARG, "x, codes and scales must be non-NULL");
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return set_error(UNO_ERR_INVALID_ARG, "x, codes and scales must be 16-byte aligned");
+  return fp8_quantize_launch(dt, M, K, block_rows, x, static_cast<uint8_t*>(codes), scales,
+                             (K + 127) / 128, 1, as_stream(stream));
+}
+
+size_t uno_gated_lora_linear_fp8_workspace(int64_t M, int64_t K, int64_t N, int32_t r) {
+  if (M < 0 || K < 1 || N < 1 || r < 0) return 0;
+  return fp8_layout(M, K, N, r, false).total;
+}
+
+uno_status uno_gated_lora_linear_fp8(uno_dtype dt, int64_t M, int64_t K, int64_t N, int32_t r,
+                                     const void* x, const void* Wq, const float* Ws, const void* A,
+                                     const void* Bl, const uint8_t* gate, float scale, void* y,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+  const uno_status s = check_fp8(dt, M, K, N, r, "K", "N");
+  if (s != UNO_OK || M == 0) return s;
+  return run_fp8(M, K, N, r, x, Wq, Ws, A, Bl, gate, scale, y, workspace, ws_bytes, false,
+                 as_stream(stream));
+}
+
+size_t uno_gated_lora_input_grad_fp8_workspace(int64_t M, int64_t K, int64_t N, int32_t r) {
+  if (M < 0 || K < 1 || N < 1 || r < 0) return 0;
+  return fp8_layout(M, N, K, r, true).total;
+}
+
+uno_status uno_gated_lora_input_grad_fp8(uno_dtype dt, int64_t M, int64_t K, int64_t N, int32_t r,
+                                         const void* dy, const void* Wqt, const float* Wst,
+                                         const void* A, const void* Bl, const uint8_t* gate,
+                                         float scale, void* dx, void* workspace, size_t ws_bytes,
+                                         void* stream) {
+  const uno_status s = check_fp8(dt, M, N, K, r, "N", "K");
+  if (s != UNO_OK || M == 0) return s;
+  return run_fp8(M, N, K, r, dy, Wqt, Wst, A, Bl, gate, scale, dx, workspace, ws_bytes, true,
+                 as_stream(stream));
+}
+
 // ---------------------------------------------------------------- sampler
 
 size_t uno_psi_verify_workspace(int32_t B, int32_t k, int32_t k_p, int32_t V) {
@@ -668,6 +824,73 @@ uno_status uno_draft_sample(uno_dtype dt, int32_t B, int32_t k, int32_t V, const
   a.draft = draft;
   a.dev_status = dev_status;
   return draft_launch(a, workspace, as_stream(stream));
+}
+
+// ---------------------------------------------------------------- logits rules
+
+uno_status uno_token_counts_add(int32_t S, int32_t V, uint16_t* counts, int32_t B, int32_t T,
+                                const int32_t* tokens, const int32_t* lens, const int32_t* slots,
+                                int32_t prompt, int32_t* dev_status, void* stream) {
+  if (S < 0 || B < 0 || T < 0) return set_error(UNO_ERR_INVALID_ARG, "bad sizes S=%d B=%d T=%d", S, B, T);
+  if (V < 2 || V > 196608) return set_error(UNO_ERR_UNSUPPORTED, "vocabulary V=%d outside [2, 196608]", V);
+  if (prompt != 0 && prompt != 1) return set_error(UNO_ERR_INVALID_ARG, "prompt must be 0 or 1");
+  if (B == 0 || T == 0) return UNO_OK;
+  if (!counts || !tokens) return set_error(UNO_ERR_INVALID_ARG, "counts and tokens must be non-NULL");
+  if (!aligned16(counts)) return set_error(UNO_ERR_INVALID_ARG, "counts must be 16-byte aligned");
+  if (!slots && S < B) return set_error(UNO_ERR_INVALID_ARG, "%d records for %d sequences without slots", S, B);
+  return token_counts_launch(counts, S, V, tokens, B, T, lens, slots, prompt != 0, dev_status,
+                             as_stream(stream));
+}
+
+uno_status uno_logits_process(uno_dtype dt, int32_t B, int32_t R, int32_t V, const void* logits, void* out,
+                              int32_t S, const uint16_t* counts, const int32_t* slots, int32_t P,
+                              int32_t path_per_row, const int32_t* path, const float* repetition,
+                              const float* frequency, const float* presence, int32_t nb,
+                              const int32_t* bias_ids, const float* bias, const uint32_t* mask,
+                              int32_t* dev_status, void* stream) {
+  if (!valid_dtype(dt)) return set_error(UNO_ERR_INVALID_ARG, "unknown dtype %d", dt);
+  if (B < 0 || R < 0 || S < 0 || P < 0 || nb < 0)
+    return set_error(UNO_ERR_INVALID_ARG, "bad sizes B=%d R=%d S=%d P=%d nb=%d", B, R, S, P, nb);
+  if (V < 2 || V > 196608) return set_error(UNO_ERR_UNSUPPORTED, "vocabulary V=%d outside [2, 196608]", V);
+  if (P > kMaxPath) return set_error(UNO_ERR_UNSUPPORTED, "path length P=%d > %d", P, kMaxPath);
+  if (nb > kMaxBias) return set_error(UNO_ERR_UNSUPPORTED, "nb=%d biases > %d", nb, kMaxBias);
+  if (path_per_row != 0 && path_per_row != 1)
+    return set_error(UNO_ERR_INVALID_ARG, "path_per_row must be 0 or 1");
+  if (B == 0 || R == 0) return UNO_OK;
+  if (!logits || !out) return set_error(UNO_ERR_INVALID_ARG, "logits and out must be non-NULL");
+  if (P > 0 && !path) return set_error(UNO_ERR_INVALID_ARG, "path must be non-NULL when P > 0");
+  if (nb > 0 && (!bias_ids || !bias))
+    return set_error(UNO_ERR_INVALID_ARG, "bias_ids and bias must be non-NULL when nb > 0");
+  if (!aligned16(logits) || !aligned16(out) || !aligned16(counts) || !aligned16(mask))
+    return set_error(UNO_ERR_INVALID_ARG, "logits, out, counts and mask must be 16-byte aligned");
+  if (counts && !slots && S < B)
+    return set_error(UNO_ERR_INVALID_ARG, "%d records for %d sequences without slots", S, B);
+  const size_t bytes = static_cast<size_t>(B) * R * V * (dt == UNO_F32 ? 4 : 2);
+  const char *i0 = static_cast<const char*>(logits), *o0 = static_cast<const char*>(out);
+  if (i0 != o0 && i0 < o0 + bytes && o0 < i0 + bytes)
+    return set_error(UNO_ERR_INVALID_ARG, "out must be logits itself or not overlap it");
+  LogitsArgs a{};
+  a.dt = dt;
+  a.B = B;
+  a.R = R;
+  a.V = V;
+  a.logits = logits;
+  a.out = out;
+  a.counts = counts;
+  a.S = S;
+  a.slots = slots;
+  a.path = P > 0 ? path : nullptr;
+  a.P = P;
+  a.path_per_row = path_per_row;
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  a.bias_ids = bias_ids;
+  a.bias = bias;
+  a.nb = nb;
+  a.mask = mask;
+  a.dev_status = dev_status;
+  return logits_process_launch(a, as_stream(stream));
 }
 
 uno_status uno_philox_uniforms(uint64_t seed, uint64_t step, uint32_t stream_id, uint32_t index0,

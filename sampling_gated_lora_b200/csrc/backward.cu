@@ -183,6 +183,15 @@ uno_status plain_gemm(int64_t rows, int64_t K, int64_t n, const void* X, const v
 
 }  // namespace
 
+uno_status transpose2_launch(const void* in0, int64_t R0, int64_t C0, void* out0, const void* in1,
+                             int64_t R1, int64_t C1, void* out1, cudaStream_t s) {
+  TransposeArgs ta{};
+  ta.scale = 1.f;
+  add_job(&ta, in0, R0, C0, C0, out0, R0, false);
+  add_job(&ta, in1, R1, C1, C1, out1, R1, false);
+  return transpose_launch(ta, s);
+}
+
 size_t adapter_backward_workspace(int64_t M, int64_t K, int64_t N, int32_t r) {
   return backward_layout(M, K, N, r).total;
 }

@@ -20,6 +20,8 @@ enum : int32_t {
   kDevBadDraft = 1,   // a draft id outside [0, V)
   kDevNaN = 2,        // a NaN among the logits of a row
   kDevTimeout = 4,    // a bounded wait gave up
+  kDevBadIndex = 8,   // a token id or a slot outside its range (skipped)
+  kDevNoToken = 16,   // a logits row whose mask allows no token
 };
 
 // Library-wide device status word (timeouts of kernels without a status

@@ -462,6 +462,25 @@ uno_status make_map(CUtensorMap* tm, uno_dtype dt, const void* base, uint64_t in
   return UNO_OK;
 }
 
+uno_status make_map_u8(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows,
+                       uint64_t row_stride_bytes, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return set_error(UNO_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {inner, rows};
+  const cuuint64_t strides[1] = {row_stride_bytes};
+  const cuuint32_t box[2] = {kRowBytes, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(UNO_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d): inner=%llu rows=%llu",
+                     static_cast<int>(r), static_cast<unsigned long long>(inner),
+                     static_cast<unsigned long long>(rows));
+  return UNO_OK;
+}
+
 int device_sm_count() {
   static int n = [] {
     int dev = 0, v = 148;

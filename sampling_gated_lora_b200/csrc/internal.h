@@ -121,6 +121,9 @@ uno_status gemm_run(const GemmLaunch& l, cudaStream_t stream);
 // Row-major [rows, inner] tensor map: box = 128 bytes of K x box_rows rows, 128-byte swizzle.
 uno_status make_map(CUtensorMap* tm, uno_dtype dt, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t row_stride_elems, uint32_t box_rows);
+// The same for rows of 8-bit values (128 of them a box).
+uno_status make_map_u8(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows,
+                       uint64_t row_stride_bytes, uint32_t box_rows);
 // The persistent CTA-pair kernel (bf16, 256x256 tiles): whether it takes the
 // problem, its preparation and its launch.
 bool gemm_pair_suits(const GemmProblem& pb);
@@ -260,6 +263,60 @@ uno_status adapter_backward_launch(int64_t M, int64_t K, int64_t N, int32_t r, c
                                    const void* dy, const void* A, const void* Bl,
                                    const uint8_t* gate, float scale, void* dA, void* dBl,
                                    void* ws, cudaStream_t s);
+
+// Block-scaled e4m3 quantisation (fp8_quantize.cu): block_rows 1 or 128. Scale of
+// row block m and column block b at scales[m * ld_m + b * ld_b] (block_rows 128:
+// dense [ceil(M/128), ceil(K/128)]).
+uno_status fp8_quantize_launch(uno_dtype dt, int64_t M, int64_t K, int block_rows, const void* x,
+                               uint8_t* q, float* scales, int64_t ld_m, int64_t ld_b,
+                               cudaStream_t s);
+
+// y [M,N] bf16 = xq wq^T under block scales + t Bl^T (fp8_gemm.cu).
+struct Fp8Gemm {
+  int64_t M, K, N;
+  int32_t r;             // 0: no adapter term
+  const void* xq;        // [M, K] e4m3
+  const float* sx;       // [ceil(K/128), ld_sx]: one scale per row and K-block, K-block major
+  int64_t ld_sx;         // M rounded up to 128
+  const void* wq;        // [N, K] e4m3
+  const float* sw;       // [ceil(N/128), ceil(K/128)]
+  const void* t;         // [M, r] bf16, gated and scaled
+  const void* Bl;        // [N, r] bf16
+  void* y;
+};
+uno_status fp8_gemm_launch(const Fp8Gemm& g, cudaStream_t s);
+
+// out_i [C_i, R_i] = in_i [R_i, C_i]^T (bf16) for two matrices in one launch
+// (backward.cu); R_i and C_i multiples of 8.
+uno_status transpose2_launch(const void* in0, int64_t R0, int64_t C0, void* out0, const void* in1,
+                             int64_t R1, int64_t C1, void* out1, cudaStream_t s);
+
+// Token records and logits rules (logits.cu), see uno_logits_process.
+constexpr int kMaxPath = 64;
+constexpr int kMaxBias = 1024;
+struct LogitsArgs {
+  uno_dtype dt;
+  int32_t B, R, V;
+  const void* logits;          // [B, R, V]
+  void* out;                   // [B, R, V], logits itself or disjoint from it
+  const uint16_t* counts;      // [S, V] or NULL
+  int32_t S;
+  const int32_t* slots;        // [B] or NULL (slot b)
+  const int32_t* path;         // [B, P] or, per row, [B, R, P]; NULL: none
+  int32_t P, path_per_row;
+  const float* repetition;     // [B] or NULL (1)
+  const float* frequency;      // [B] or NULL (0)
+  const float* presence;       // [B] or NULL (0)
+  const int32_t* bias_ids;     // [B, nb], -1: none
+  const float* bias;           // [B, nb]
+  int32_t nb;
+  const uint32_t* mask;        // [B, R, ceil(V/32)] or NULL
+  int32_t* dev_status;
+};
+uno_status logits_process_launch(const LogitsArgs& a, cudaStream_t s);
+uno_status token_counts_launch(uint16_t* counts, int32_t S, int32_t V, const int32_t* tokens, int32_t B,
+                               int32_t T, const int32_t* lens, const int32_t* slots, bool prompt,
+                               int32_t* dev_status, cudaStream_t s);
 
 // The bounded-wait self-test (waits.cu).
 uno_status wait_selftest_launch(int32_t which, uint64_t limit_ns, int32_t* result,
