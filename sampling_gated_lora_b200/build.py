@@ -3,7 +3,8 @@
     python -m sampling_gated_lora_b200.build [--force] [-j N]
 
 Every CUDA source in csrc/ is compiled for sm_100a only (relocatable device
-code, so the library-wide device status word can be shared between files)
+code, so the library-wide device status word can be shared between files, but
+for WHOLE_PROGRAM: ptxas ignores setmaxnreg in relocatable code)
 and linked into sampling_gated_lora_b200/libuno.so next to this file.
 """
 from __future__ import annotations
@@ -25,6 +26,10 @@ LIB = os.path.join(HERE, "libuno.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-rdc=true", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
+
+
+# sources compiled without relocatable device code (they use setmaxnreg)
+WHOLE_PROGRAM = {"fp8_gemm.cu"}
 
 
 def nvcc() -> str:
@@ -55,7 +60,9 @@ def up_to_date() -> bool:
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-    cmd = [nvcc(), *ARCH, *NVCC_FLAGS, "-I", INCLUDE, "-c", src, "-o", obj]
+    flags = [f for f in NVCC_FLAGS
+             if f != "-rdc=true" or os.path.basename(src) not in WHOLE_PROGRAM]
+    cmd = [nvcc(), *ARCH, *flags, "-I", INCLUDE, "-c", src, "-o", obj]
     if verbose:
         cmd += ["-Xptxas", "-v"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -4,6 +4,7 @@
 #include <cstdlib>
 #include <cstdio>
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <memory>
 #include <mutex>
@@ -43,6 +44,23 @@ bool pdl_enabled() {
     return !(v && v[0] == '0');
   }();
   return on;
+}
+
+int32_t* device_status_word() {
+  constexpr int kDevices = 64;
+  static std::atomic<int32_t*> word[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev >= 0 && dev < kDevices)
+    if (int32_t* w = word[dev].load(std::memory_order_acquire)) return w;
+  void* p = nullptr;
+  if (e == cudaSuccess) e = cudaGetSymbolAddress(&p, g_device_status);
+  if (e != cudaSuccess) {
+    cuda_error(e, "address of the device status word");
+    return nullptr;
+  }
+  if (dev >= 0 && dev < kDevices) word[dev].store(static_cast<int32_t*>(p), std::memory_order_release);
+  return static_cast<int32_t*>(p);
 }
 
 uno_status cuda_error(cudaError_t e, const char* what) {
@@ -432,6 +450,7 @@ uno_status run_fp8(int64_t M, int64_t Kc, int64_t No, int32_t r, const void* x, 
   g.t = base + L.t;
   g.Bl = Bl;
   g.y = y;
+  if (!(g.status = device_status_word())) return UNO_ERR_CUDA;
   return fp8_gemm_launch(g, st);
 }
 

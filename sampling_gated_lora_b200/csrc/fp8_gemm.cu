@@ -25,7 +25,6 @@ namespace uno {
 
 namespace {
 
-constexpr int kThreads = 192;
 constexpr int kRows = 128;                           // features per tile (MMA M)
 constexpr uint32_t kWBytes = kRows * 128;            // one 128-row, 128-byte K-block tile
 constexpr int kPartPad = 4;
@@ -42,48 +41,109 @@ struct Fp8Params {
   const float* sx;
   const float* sw;
   __nv_bfloat16* y;
+  int32_t* status;           // library-wide device status word
 };
+
+// This file is compiled without relocatable device code (setmaxnreg needs it),
+// so the status word comes as a pointer.
+__device__ __forceinline__ void raise_timeout(int32_t* status) { atomicOr(status, kDevTimeout); }
+
+// Position in a ring of N slots and the parity of the current pass over it
+// (a running counter: one thread issues every copy and every MMA, and a
+// division by the ring's size a K-block would be on its critical path).
+struct Ring {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// acc[i] += f * v[i] and acc[i+1] += g * v[i+1], one packed instruction (the
+// epilogue's adds are on the path that frees a TMEM buffer: 380 -> 355 us at
+// 4352 x 12288 -> 4096 against scalar adds).
+__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t v1, uint64_t fg) {
+  uint64_t a, v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(fg));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 // ---------------------------------------------------------------- few tokens
 // Weights on the 128-row MMA side, BN tokens on the N side: a lane of TMEM is
-// a feature and a column a token. K is split over a thread-block cluster so
-// that every SM streams a share of W (HBM bandwidth bounds these sizes); the
-// CTAs' fp32 sums meet through distributed shared memory, in rank order.
+// a feature and a column a token. HBM bandwidth bounds these sizes, so W is
+// read once. With fewer tiles than SMs, K is split over a thread-block cluster
+// so that every SM streams a share, and the CTAs' fp32 sums meet through
+// distributed shared memory in rank order; otherwise each CTA walks whole
+// tiles, and the stores of one overlap the loads and products of the next.
+// Up to 64 tokens four epilogue warps hold the sums, from 128 on eight (halves
+// of the columns); the factors of a column's token are staged per warp in
+// shared memory and read as broadcasts.
 template <int BN>
 struct Narrow {
   static constexpr uint32_t kStage = kWBytes + BN * 128;
   static constexpr int kStride = BN < 32 ? 32 : BN;      // TMEM columns of a buffer
-  static constexpr int kBufs = BN <= 64 ? 8 : 4;
+  static constexpr int kBufs = BN <= 64 ? 8 : 512 / BN;
   static constexpr int kCols = kStride * kBufs;
+  static constexpr int kEpi = BN <= 64 ? 4 : 8;          // epilogue warps
+  static constexpr int kFirst = BN <= 64 ? 2 : 4;        // the first of them
+  static constexpr int kCW = BN * 4 / kEpi;              // columns of an epilogue warp
+  static constexpr int kThreads = 32 * (kFirst + kEpi);
+  static constexpr bool kMoveRegs = BN == 256;           // see kPairThreads
+  // Scales are copied to shared memory kSlots - 1 K-blocks ahead: an L2 read
+  // takes longer than a block of 16 KB of W does at HBM rate (0.36 us an SM).
+  static constexpr int kSlots = BN <= 64 ? 8 : 4;
 };
 
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int BN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
     fp8_narrow_kernel(const __grid_constant__ Fp8Maps tm, const Fp8Params p) {
   using C = Narrow<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023u) & ~static_cast<uintptr_t>(1023u));
-  __shared__ float fac[4][2][BN];                        // per epilogue warp: factors of one K-block
-  __shared__ uint64_t accf[C::kBufs], acce[C::kBufs];
+  // per epilogue warp: factors of the K-blocks in use, scales (tokens', W's) of those ahead
+  __shared__ alignas(16) float fac[C::kEpi][2][C::kCW];
+  __shared__ float scl[C::kEpi][C::kSlots][C::kCW + 1];
+  __shared__ uint64_t acce[C::kBufs];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   const int S = p.stages;
+  // full: a stage has been filled; done: the MMAs on it have completed (frees the
+  // stage to the producer and shows the block's sum to the epilogue, which is
+  // never more than kBufs <= S blocks behind, so it sees every phase); acce: a
+  // TMEM buffer has been read
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * C::kStage);
-  uint64_t* empty = full + S;
+  uint64_t* done = full + S;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tok0 = blockIdx.x * BN, feat0 = blockIdx.y * kRows;
+  const int tok_tiles = (p.M + BN - 1) / BN;
+  const int tiles = tok_tiles * ((p.N + kRows - 1) / kRows);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&done[s]), 1);
     }
-    for (int b = 0; b < C::kBufs; ++b) {
-      mbar_init(smem_u32(&accf[b]), 1);
-      mbar_init(smem_u32(&acce[b]), 4);
-    }
+    for (int b = 0; b < C::kBufs; ++b) mbar_init(smem_u32(&acce[b]), C::kEpi);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -97,157 +157,222 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   if (threadIdx.x == 0) pdl_trigger();
 
+  const int nkb = p.nkb + p.nkr;
   const int kb0 = blockIdx.z * p.kb_per_split;
-  const int kb1 = min(p.nkb + p.nkr, kb0 + p.kb_per_split);
+  const int kb1 = min(nkb, kb0 + p.kb_per_split);
+  const int step = gridDim.x;   // splits > 1: one tile per cluster
   auto fail = [&]() {
     abort_flag = 1;
-    raise_status(nullptr, kDevTimeout);
+    raise_timeout(p.status);
   };
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------------------ TMA producer
-    auto load_w = [&](int kb, uint32_t st, uint32_t fb) {
-      if (kb < p.nkb) tma_load_2d(st, &tm.w, kb * 128, feat0, fb);
-      else tma_load_2d(st, &tm.b, (kb - p.nkb) * 64, feat0, fb);
-    };
-    auto load_x = [&](int kb, uint32_t st, uint32_t fb) {
-      if (kb < p.nkb) tma_load_2d(st + kWBytes, &tm.x, kb * 128, tok0, fb);
-      else tma_load_2d(st + kWBytes, &tm.t, (kb - p.nkb) * 64, tok0, fb);
-    };
-    // weights (constant) of the first stages before waiting for the writer of xq and t
-    const int pre = min(S, kb1 - kb0);
-    for (int q = 0; q < pre; ++q) {
-      mbar_arrive_expect_tx(smem_u32(&full[q]), C::kStage);
-      load_w(kb0 + q, smem_u32(smem + q * C::kStage), smem_u32(&full[q]));
-    }
-    pdl_wait();
-    for (int q = 0; q < pre; ++q)
-      load_x(kb0 + q, smem_u32(smem + q * C::kStage), smem_u32(&full[q]));
-    int it = pre;
-    for (int kb = kb0 + pre; kb < kb1; ++kb, ++it) {
-      const int s = it % S;
-      if (!mbar_wait(smem_u32(&empty[s]), ((it / S) & 1u) ^ 1u) || abort_flag) {
-        fail();
-        break;
+  if (warp < C::kFirst) {
+    if (C::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- TMA producer
+      auto load_w = [&](int tile, int kb, uint32_t st, uint32_t fb) {
+        const int feat0 = tile / tok_tiles * kRows;
+        if (kb < p.nkb) tma_load_2d(st, &tm.w, kb * 128, feat0, fb);
+        else tma_load_2d(st, &tm.b, (kb - p.nkb) * 64, feat0, fb);
+      };
+      auto load_x = [&](int tile, int kb, uint32_t st, uint32_t fb) {
+        const int tok0 = tile % tok_tiles * BN;
+        if (kb < p.nkb) tma_load_2d(st + kWBytes, &tm.x, kb * 128, tok0, fb);
+        else tma_load_2d(st + kWBytes, &tm.t, (kb - p.nkb) * 64, tok0, fb);
+      };
+      // weights (constant) of the first stages before waiting for the writer of xq and t
+      const int pre = min(S, kb1 - kb0);
+      for (int q = 0; q < pre; ++q) {
+        mbar_arrive_expect_tx(smem_u32(&full[q]), C::kStage);
+        load_w(blockIdx.x, kb0 + q, smem_u32(smem + q * C::kStage), smem_u32(&full[q]));
       }
-      const uint32_t st = smem_u32(smem + s * C::kStage), fb = smem_u32(&full[s]);
-      mbar_arrive_expect_tx(fb, C::kStage);
-      load_w(kb, st, fb);
-      load_x(kb, st, fb);
-    }
-  } else if (warp == 1 && lane == 0) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t id8 = idesc_e4m3(kRows, BN), id16 = idesc_f32acc(kRows, BN, false);
-    int it = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-      const int s = it % S, b = it % C::kBufs;
-      if (!mbar_wait(smem_u32(&acce[b]), ((it / C::kBufs) & 1u) ^ 1u) ||
-          !mbar_wait(smem_u32(&full[s]), (it / S) & 1u)) {
-        fail();
-        break;
-      }
-      tc_fence_after();
-      const uint32_t st = smem_u32(smem + s * C::kStage);
-      const uint64_t wd = sdesc_k_sw128(st), xd = sdesc_k_sw128(st + kWBytes);
-      const uint32_t d = tmem + static_cast<uint32_t>(b * C::kStride);
-      if (kb < p.nkb) {
+      pdl_wait();
+      for (int q = 0; q < pre; ++q)
+        load_x(blockIdx.x, kb0 + q, smem_u32(smem + q * C::kStage), smem_u32(&full[q]));
+      Ring st;
+      for (int q = 0; q < pre; ++q) st.next(S);
+      int skip = pre;   // blocks of the first tile that are on their way
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += step, skip = 0)
+        for (int kb = kb0 + skip; kb < kb1; ++kb, st.next(S)) {
+          if (!mbar_wait(smem_u32(&done[st.i]), st.ph ^ 1u) || abort_flag) {
+            fail();
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem_u32(smem + st.i * C::kStage), fb = smem_u32(&full[st.i]);
+          mbar_arrive_expect_tx(fb, C::kStage);
+          load_w(tile, kb, sa, fb);
+          load_x(tile, kb, sa, fb);
+        }
+    } else if (warp == 1 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t id8 = idesc_e4m3(kRows, BN), id16 = idesc_f32acc(kRows, BN, false);
+      Ring st, buf;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += step)
+        for (int kb = kb0; kb < kb1; ++kb, st.next(S), buf.next(C::kBufs)) {
+          if (!mbar_wait(smem_u32(&acce[buf.i]), buf.ph ^ 1u) || !mbar_wait(smem_u32(&full[st.i]), st.ph)) {
+            fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + static_cast<uint32_t>(buf.i * C::kStride);
+          const uint32_t sa = smem_u32(smem + st.i * C::kStage);
+          const uint64_t wd = sdesc_k_sw128(sa), xd = sdesc_k_sw128(sa + kWBytes);
+          if (kb < p.nkb) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_f8(d, wd + 2 * kk, xd + 2 * kk, id8, kk > 0 ? 1u : 0u);
-      } else {
+            for (int kk = 0; kk < 4; ++kk) mma_f8(d, wd + 2 * kk, xd + 2 * kk, id8, kk > 0 ? 1u : 0u);
+          } else {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss<false>(d, wd + 2 * kk, xd + 2 * kk, id16, kk > 0 ? 1u : 0u);
-      }
-      mma_commit(smem_u32(&empty[s]));
-      mma_commit(smem_u32(&accf[b]));
+            for (int kk = 0; kk < 4; ++kk) mma_ss<false>(d, wd + 2 * kk, xd + 2 * kk, id16, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(smem_u32(&done[st.i]));
+        }
     }
-  } else if (warp >= 2) {
+  } else {
     // ------------------------------------------------------------ block sums -> registers
-    const int quarter = warp & 3;
-    const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    float(*fw)[BN] = fac[quarter];
-    const float* sw = p.sw + static_cast<size_t>(blockIdx.y) * p.ld_sw;
-    constexpr int kPer = (BN + 31) / 32;
-    auto factor = [&](int kb, float (&f)[kPer]) {   // this lane's tokens' factors of K-block kb
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int j = lane + 32 * i;
-        f[i] = 1.f;
-        if (kb < p.nkb && j < BN)
-          f[i] = p.sx[static_cast<size_t>(kb) * p.ld_sx + tok0 + j] * sw[kb];
-      }
-    };
-    float acc[BN];
-#pragma unroll
-    for (int j = 0; j < BN; ++j) acc[j] = 0.f;
+    if (C::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    constexpr int kCW = C::kCW, kPer = (kCW + 31) / 32, kChunk = kCW < 32 ? kCW : 32;
+    const int quarter = warp & 3, half = (warp - C::kFirst) >> 2;
+    const uint32_t tcol = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kCW);
+    float(*fw)[kCW] = fac[warp - C::kFirst];
+    const int groups = kb1 - kb0;
     pdl_wait();
-    float f[kPer];
-    factor(kb0, f);
-    int it = 0;
-    bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-      const int b = it % C::kBufs;
-      float* fs = fw[it & 1];
+    // copy the scales of K-block ahead_g of tile ahead_tile (factor 1 for the adapter's)
+    constexpr int kSlots = C::kSlots;
+    float(*sl)[kCW + 1] = scl[warp - C::kFirst];
+    int ahead_tile = blockIdx.x, ahead_g = 0, ahead = 0;
+    auto prefetch = [&]() {
+      if (ahead_tile < tiles) {
+        float* dst = sl[ahead % kSlots];
+        const int kb = kb0 + ahead_g, t0 = ahead_tile % tok_tiles * BN + half * kCW;
+        const bool main = kb < p.nkb;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (lane + 32 * i < BN) fs[lane + 32 * i] = f[i];
-      if (kb + 1 < kb1) factor(kb + 1, f);
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&accf[b]), (it / C::kBufs) & 1u));
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < BN; c += 16) {
-        float v[16];
-        tmem_ld16(trow + static_cast<uint32_t>(b * C::kStride + c), v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(fs[c + j], v[j], acc[c + j]);
+        for (int i = 0; i < kPer; ++i) {
+          const int j = lane + 32 * i;
+          if (j < kCW) {
+            if (main && t0 + j < p.ld_sx) copy_async4(smem_u32(dst + j), p.sx + static_cast<size_t>(kb) * p.ld_sx + t0 + j);
+            else dst[j] = 1.f;
+          }
+        }
+        if (lane == 0) {
+          if (main) copy_async4(smem_u32(dst + kCW), p.sw + static_cast<size_t>(ahead_tile / tok_tiles) * p.ld_sw + kb);
+          else dst[kCW] = 1.f;
+        }
+        if (++ahead_g == groups) {
+          ahead_g = 0;
+          ahead_tile += step;
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&acce[b]));
+      ++ahead;
+      copy_async_commit();
+    };
+    for (int i = 0; i < kSlots - 1; ++i) prefetch();
+    int grp = 0;
+    Ring st, buf;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += step) {
+      const int tok0 = tile % tok_tiles * BN + half * kCW, feat0 = tile / tok_tiles * kRows;
+      float acc[kCW];
+#pragma unroll
+      for (int j = 0; j < kCW; ++j) acc[j] = 0.f;
+      for (int g = 0; g < groups; ++g, ++grp, st.next(S), buf.next(C::kBufs)) {
+        float* f = fw[grp & 1];
+        const float* in = sl[grp % kSlots];
+        copy_async_wait<kSlots - 2>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (lane + 32 * i < kCW) f[lane + 32 * i] = in[lane + 32 * i] * in[kCW];
+        __syncwarp();
+        prefetch();
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&done[st.i]), st.ph));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t0 = tcol + static_cast<uint32_t>(buf.i * C::kStride);
+        uint32_t v[2][kChunk];
+        tmem_ld_async(t0, v[0]);
+#pragma unroll
+        for (int c = 0; c < kCW; c += kChunk) {
+          uint32_t(&w)[kChunk] = v[(c / kChunk) & 1];
+          tmem_wait_ld(w);
+          if (c + kChunk < kCW) {
+            tmem_ld_async(t0 + c + kChunk, v[(c / kChunk + 1) & 1]);
+          } else {   // the buffer has been read: hand it back to the MMA issuer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&acce[buf.i]));
+          }
+#pragma unroll
+          for (int j = 0; j < kChunk; j += 4) {
+            const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(f + c + j);
+            fma2(acc[c + j], acc[c + j + 1], w[j], w[j + 1], q.x);
+            fma2(acc[c + j + 2], acc[c + j + 3], w[j + 2], w[j + 3], q.y);
+          }
+        }
+      }
+      if (!ok) break;
+      if (p.splits > 1) {
+        // every MMA has finished, so the stage ring is free: stage the sums [token][feature]
+        float* stage = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int j = 0; j < kCW; ++j)
+          stage[(half * kCW + j) * (kRows + kPartPad) + quarter * 32 + lane] = acc[j];
+      } else {
+        // lanes hold features, so pairs of lanes swap halves of two tokens and
+        // store two features each
+        const int n = feat0 + quarter * 32 + (lane & ~1);
+#pragma unroll
+        for (int j = 0; j < kCW; j += 2) {
+          if (tok0 + j >= p.M) break;
+          const bool odd = lane & 1;
+          const float other = __shfl_xor_sync(0xffffffffu, odd ? acc[j] : acc[j + 1], 1);
+          const int m = tok0 + j + odd;
+          const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(other, acc[j + 1]) : __floats2bfloat162_rn(acc[j], other);
+          if (m < p.M && n < p.N) *reinterpret_cast<__nv_bfloat162*>(p.y + static_cast<size_t>(m) * p.N + n) = o;
+        }
+      }
     }
     if (!ok && lane == 0) fail();
-    // every MMA has finished, so the stage ring is free: stage the sums [token][feature]
-    float* stage = reinterpret_cast<float*>(smem);
-    if (ok) {
-#pragma unroll
-      for (int j = 0; j < BN; ++j) stage[j * (kRows + kPartPad) + quarter * 32 + lane] = acc[j];
-    }
   }
 
-  if (p.splits > 1) cluster_sync_converged();
-  else cta_sync_converged();
-  if (!abort_flag) {
-    // the CTAs of the cluster share the tile's outputs out, 4 features at a time
-    constexpr int kGroups = BN * (kRows / 4);
-    const int Sp = p.splits;
-    const int chunk = (kGroups + Sp - 1) / Sp;
-    const int e0 = static_cast<int>(cluster_ctarank()) * chunk, e1 = min(kGroups, e0 + chunk);
-    const uint32_t part0 = smem_u32(smem);
-    uint32_t peer[8];
+  if (p.splits > 1) {
+    cluster_sync_converged();
+    if (!abort_flag) {
+      // the CTAs of the cluster share the tile's outputs out, 4 features at a time
+      const int tok0 = static_cast<int>(blockIdx.x) % tok_tiles * BN, feat0 = static_cast<int>(blockIdx.x) / tok_tiles * kRows;
+      constexpr int kGroups = BN * (kRows / 4);
+      const int Sp = p.splits;
+      const int chunk = (kGroups + Sp - 1) / Sp;
+      const int e0 = static_cast<int>(cluster_ctarank()) * chunk, e1 = min(kGroups, e0 + chunk);
+      const uint32_t part0 = smem_u32(smem);
+      uint32_t peer[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) peer[r] = map_shared_rank(part0, r < Sp ? r : 0);
-    for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += kThreads) {
-      const int j = e / (kRows / 4), i4 = e % (kRows / 4);
-      const int m = tok0 + j, n = feat0 + 4 * i4;
-      if (m >= p.M || n >= p.N) continue;
-      const uint32_t off = static_cast<uint32_t>((j * (kRows + kPartPad) + 4 * i4) * 4);
-      float4 v[8];
+      for (int r = 0; r < 8; ++r) peer[r] = map_shared_rank(part0, r < Sp ? r : 0);
+      for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += C::kThreads) {
+        const int j = e / (kRows / 4), i4 = e % (kRows / 4);
+        const int m = tok0 + j, n = feat0 + 4 * i4;
+        if (m >= p.M || n >= p.N) continue;
+        const uint32_t off = static_cast<uint32_t>((j * (kRows + kPartPad) + 4 * i4) * 4);
+        float4 v[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < Sp) v[r] = ld_cluster_f32x4(peer[r] + off);
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < 8; ++r)
+          if (r < Sp) v[r] = ld_cluster_f32x4(peer[r] + off);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < Sp) {
-          a.x += v[r].x; a.y += v[r].y; a.z += v[r].z; a.w += v[r].w;
-        }
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
-      *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(m) * p.N + n) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        for (int r = 0; r < 8; ++r)
+          if (r < Sp) {
+            a.x += v[r].x; a.y += v[r].y; a.z += v[r].z; a.w += v[r].w;
+          }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
+        *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(m) * p.N + n) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
     }
+    cluster_sync_converged();   // the peers have read this CTA's sums
   }
-  if (p.splits > 1) cluster_sync_converged();   // the peers have read this CTA's sums
 
   tc_fence_before();
   cta_sync_converged();
@@ -261,20 +386,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int BN>
 uno_status narrow_launch(const Fp8Maps& tm, Fp8Params p, cudaStream_t s) {
   using C = Narrow<BN>;
-  const int tok_tiles = (p.M + BN - 1) / BN, feat_tiles = (p.N + kRows - 1) / kRows;
-  if (feat_tiles > 65535) return set_error(UNO_ERR_UNSUPPORTED, "N too large for the tile grid");
-  p.stages = std::min(8, static_cast<int>(200u * 1024u / C::kStage));
+  const int64_t tiles = static_cast<int64_t>((p.M + BN - 1) / BN) * ((p.N + kRows - 1) / kRows);
+  if (tiles > (1ll << 30)) return set_error(UNO_ERR_UNSUPPORTED, "too many tiles");
+  p.stages = std::min(12, static_cast<int>(196u * 1024u / C::kStage));
   const int smem = static_cast<int>(p.stages * (C::kStage + 16) + 1024);
-  const int nkb = p.nkb + p.nkr;
-  int splits = std::max(1, std::min({8, device_sm_count() / std::max(1, tok_tiles * feat_tiles), nkb}));
+  const int nkb = p.nkb + p.nkr, sms = device_sm_count();
+  int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, sms / tiles, nkb})));
   p.kb_per_split = (nkb + splits - 1) / splits;
   p.splits = splits = (nkb + p.kb_per_split - 1) / p.kb_per_split;
   auto fn = &fp8_narrow_kernel<BN>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(8-bit GEMM smem)");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(tok_tiles, feat_tiles, splits);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? tiles : std::min<int64_t>(tiles, sms)), 1, splits);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -282,6 +407,234 @@ uno_status narrow_launch(const Fp8Maps& tm, Fp8Params p, cudaStream_t s) {
   cfg.attrs = attr;
   e = cudaLaunchKernelEx(&cfg, fn, tm, p);
   return e == cudaSuccess ? UNO_OK : cuda_error(e, "8-bit GEMM launch");
+}
+
+// ---------------------------------------------------------------- many tokens
+// A CTA pair (cta_group::2) computes 256 x 256 tiles: CTA r holds tokens
+// [128 r, 128 r + 128) of the A side and features [128 r, 128 r + 128) of the B
+// side, its TMEM its 128 token rows over all 256 features. The sum of one
+// K-block takes a 256-column buffer; two buffers alternate, so while the tensor
+// core works on block b (512 cycles at the full e4m3 rate) the eight epilogue
+// warps of each CTA add block b - 1 into their registers: a lane has one token
+// row and 128 features (one weight scale), i.e. one factor and 128 fused adds a
+// block, 256 cycles an SM sub-partition.
+// Roles of the 384 threads: warp 0 TMA producer (both CTAs), warp 1 MMA issuer
+// (leader), warps 2 and 3 idle, warps 4..11 epilogue (warp % 4: TMEM lanes, (warp - 4)
+// / 4: features). The launch gives every thread 168 registers; the first
+// warpgroup hands all but 56 of its own to the two epilogue warpgroups, whose
+// 128 sums a thread need more (128 (56 + 2 * 224) = 384 * 168).
+constexpr int kPairThreads = 384;
+constexpr uint32_t kPairStage = 2 * kWBytes;
+constexpr int kPairStages = 6;
+constexpr int kPairTile = 256;
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ Fp8Maps tm, const Fp8Params p) {
+  constexpr int S = kPairStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023u) & ~static_cast<uintptr_t>(1023u));
+  __shared__ uint64_t full[S], done[S], acce[2];   // as in the kernel above
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  const int tiles_m = (p.M + kPairTile - 1) / kPairTile;
+  const int num_tiles = tiles_m * ((p.N + kPairTile - 1) / kPairTile);
+  const int nkb = p.nkb + p.nkr;   // stages of a tile
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&done[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&acce[b]), 16);   // 8 epilogue warps x 2 CTAs
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(smem_u32(&tmem_slot), 2 * kPairTile);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (threadIdx.x == 0) pdl_trigger();
+  auto fail = [&]() {
+    abort_flag = 1;
+    raise_timeout(p.status);
+  };
+
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    Ring st;
+    bool ok = true, waited = false;
+    for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+      const int m0 = (tile % tiles_m) * kPairTile + static_cast<int>(rank) * 128;
+      const int n0 = (tile / tiles_m) * kPairTile + static_cast<int>(rank) * 128;
+      auto load_x = [&](int kb, uint32_t sa, uint32_t fb) {
+        if (kb < p.nkb) tma_load_2d_pair(sa, &tm.x, kb * 128, m0, fb);
+        else tma_load_2d_pair(sa, &tm.t, (kb - p.nkb) * 64, m0, fb);
+      };
+      auto load_w = [&](int kb, uint32_t sa, uint32_t fb) {
+        if (kb < p.nkb) tma_load_2d_pair(sa + kWBytes, &tm.w, kb * 128, n0, fb);
+        else tma_load_2d_pair(sa + kWBytes, &tm.b, (kb - p.nkb) * 64, n0, fb);
+      };
+      int kb = 0;
+      if (!waited) {   // weights (constant) of the first stages before waiting for xq and t
+        const int pre = min(S, nkb);
+        for (int q = 0; q < pre; ++q) {
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full[q]), 2 * kPairStage);
+          load_w(q, smem_u32(smem + q * kPairStage), map_shared_rank(smem_u32(&full[q]), 0));
+        }
+        pdl_wait();
+        waited = true;
+        for (; kb < pre; ++kb, st.next(S))
+          load_x(kb, smem_u32(smem + kb * kPairStage), map_shared_rank(smem_u32(&full[kb]), 0));
+      }
+      for (; kb < nkb; ++kb, st.next(S)) {
+        if (!mbar_wait(smem_u32(&done[st.i]), st.ph ^ 1u) || abort_flag) {
+          fail();
+          ok = false;
+          break;
+        }
+        const uint32_t fb = map_shared_rank(smem_u32(&full[st.i]), 0);
+        const uint32_t sa = smem_u32(smem + st.i * kPairStage);
+        if (leader) mbar_arrive_expect_tx(smem_u32(&full[st.i]), 2 * kPairStage);
+        load_x(kb, sa, fb);
+        load_w(kb, sa, fb);
+      }
+    }
+    if (!waited) pdl_wait();
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    const uint32_t id8 = idesc_e4m3(kPairTile, kPairTile), id16 = idesc_f32acc(kPairTile, kPairTile, false);
+    Ring st, buf;
+    bool ok = true;
+    for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+      for (int kb = 0; kb < nkb; ++kb, st.next(S), buf.next(2)) {
+        if (!mbar_wait_cluster(smem_u32(&acce[buf.i]), buf.ph ^ 1u) || !mbar_wait(smem_u32(&full[st.i]), st.ph)) {
+          fail();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(buf.i * kPairTile);
+        const uint32_t sa = smem_u32(smem + st.i * kPairStage);
+        const uint64_t ad = sdesc_k_sw128(sa), bd = sdesc_k_sw128(sa + kWBytes);
+        if (kb < p.nkb) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_pair_f8(d, ad + 2 * kk, bd + 2 * kk, id8, kk > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_pair_bf16(d, ad + 2 * kk, bd + 2 * kk, id16, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_both(smem_u32(&done[st.i]));
+      }
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ------------------------------------------------------------ block sums -> registers (both CTAs)
+    const int quarter = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t tcol = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(h * 128);
+    Ring st, buf;
+    bool ok = true;
+    pdl_wait();
+    for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+      const int m = (tile % tiles_m) * kPairTile + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      const int n0 = (tile / tiles_m) * kPairTile + h * 128;
+      const bool have_m = m < p.ld_sx, have_n = n0 < p.N;
+      const float* sx = p.sx + (have_m ? m : 0);
+      const float* sw = p.sw + (have_n ? static_cast<size_t>(n0 >> 7) * p.ld_sw : 0);
+      // a block's two scales are loaded two blocks ahead and multiplied when they
+      // are used (a product any earlier would stall on the loads)
+      auto load_x = [&](int g) { return g < p.nkb ? sx[static_cast<size_t>(g) * p.ld_sx] : 1.f; };
+      auto load_w = [&](int g) { return g < p.nkb ? sw[g] : 1.f; };
+      float fx[2] = {load_x(0), load_x(1)}, fw[2] = {load_w(0), load_w(1)};
+      float acc[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+      for (int g = 0; g < nkb; ++g, st.next(S), buf.next(2)) {
+        const float f = fx[0] * fw[0];
+        fx[0] = fx[1];
+        fw[0] = fw[1];
+        fx[1] = load_x(g + 2);
+        fw[1] = load_w(g + 2);
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&done[st.i]), st.ph));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t0 = tcol + static_cast<uint32_t>(buf.i * kPairTile);
+        uint32_t v[2][32];
+        const uint64_t ff = pack2(f, f);
+        auto add = [&](int c) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            fma2(acc[32 * c + j], acc[32 * c + j + 1], v[c & 1][j], v[c & 1][j + 1], ff);
+        };
+        // only half of the adds stand before the buffer is handed back
+        tmem_ld_async(t0, v[0]);
+        tmem_ld_async(t0 + 32, v[1]);
+        tmem_wait_ld(v[0]);
+        tmem_wait_ld(v[1]);
+        add(0);
+        tmem_ld_async(t0 + 64, v[0]);
+        add(1);
+        tmem_ld_async(t0 + 96, v[1]);
+        tmem_wait_ld(v[0]);
+        tmem_wait_ld(v[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_shared_rank(smem_u32(&acce[buf.i]), 0));
+        add(2);
+        add(3);
+      }
+      if (!ok) {
+        if (lane == 0) fail();
+        break;
+      }
+      if (m < p.M) {
+        __nv_bfloat16* y = p.y + static_cast<size_t>(m) * p.N + n0;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          if (n0 + c >= p.N) break;
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 q = __floats2bfloat162_rn(acc[c + 2 * e], acc[c + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&q);
+          }
+          *reinterpret_cast<uint4*>(y + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync_converged();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * kPairTile);
+  }
+}
+
+uno_status pair_launch(const Fp8Maps& tm, const Fp8Params& p, cudaStream_t s) {
+  const int64_t tiles = static_cast<int64_t>((p.M + kPairTile - 1) / kPairTile) *
+                        ((p.N + kPairTile - 1) / kPairTile);
+  if (tiles > (1ll << 30)) return set_error(UNO_ERR_UNSUPPORTED, "too many tiles");
+  const int pairs = static_cast<int>(std::min<int64_t>(std::max(1, device_sm_count() / 2), tiles));
+  const int smem = static_cast<int>(kPairStages * kPairStage + 1024);
+  cudaError_t e = cudaFuncSetAttribute(&fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(8-bit pair smem)");
+  e = launch_kernel(fp8_pair_kernel, dim3(2 * pairs), dim3(kPairThreads), smem, s, 2, tm, p);
+  return e == cudaSuccess ? UNO_OK : cuda_error(e, "8-bit pair GEMM launch");
 }
 
 }  // namespace
@@ -297,22 +650,27 @@ uno_status fp8_gemm_launch(const Fp8Gemm& g, cudaStream_t s) {
   p.sx = g.sx;
   p.sw = g.sw;
   p.y = static_cast<__nv_bfloat16*>(g.y);
-  const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+  p.status = g.status;
+  const bool pair = g.M > 256;
+  const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : g.M <= 128 ? 128 : 256;
+  const int xbox = pair ? 128 : bn;
   Fp8Maps tm;
   uno_status st;
-  if ((st = make_map_u8(&tm.x, g.xq, g.K, g.M, g.K, bn)) != UNO_OK) return st;
+  if ((st = make_map_u8(&tm.x, g.xq, g.K, g.M, g.K, xbox)) != UNO_OK) return st;
   if ((st = make_map_u8(&tm.w, g.wq, g.K, g.N, g.K, kRows)) != UNO_OK) return st;
   tm.t = tm.x;
   tm.b = tm.w;
   if (g.r > 0) {
-    if ((st = make_map(&tm.t, UNO_BF16, g.t, g.r, g.M, g.r, bn)) != UNO_OK) return st;
+    if ((st = make_map(&tm.t, UNO_BF16, g.t, g.r, g.M, g.r, xbox)) != UNO_OK) return st;
     if ((st = make_map(&tm.b, UNO_BF16, g.Bl, g.r, g.N, g.r, kRows)) != UNO_OK) return st;
   }
+  if (pair) return pair_launch(tm, p, s);
   switch (bn) {
     case 16: return narrow_launch<16>(tm, p, s);
     case 32: return narrow_launch<32>(tm, p, s);
     case 64: return narrow_launch<64>(tm, p, s);
-    default: return narrow_launch<128>(tm, p, s);
+    case 128: return narrow_launch<128>(tm, p, s);
+    default: return narrow_launch<256>(tm, p, s);
   }
 }
 

@@ -283,6 +283,7 @@ struct Fp8Gemm {
   const void* t;         // [M, r] bf16, gated and scaled
   const void* Bl;        // [N, r] bf16
   void* y;
+  int32_t* status;       // device_status_word()
 };
 uno_status fp8_gemm_launch(const Fp8Gemm& g, cudaStream_t s);
 
@@ -323,6 +324,9 @@ uno_status wait_selftest_launch(int32_t which, uint64_t limit_ns, int32_t* resul
                                 int32_t* status, cudaStream_t s);
 
 int device_sm_count();
+// Address of the library-wide status word on the current device (NULL and an
+// error set when it cannot be had).
+int32_t* device_status_word();
 
 // Launch attributes shared by every kernel launch: programmatic stream
 // serialisation (unless UNO_PDL=0 in the environment) and, when cluster_x *
