@@ -150,13 +150,19 @@ def _check(st: int):
 
 # ---------------------------------------------------------------- marshalling helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, device=None):
@@ -164,10 +170,12 @@ def _stream(stream, device=None):
     explicit stream must belong to `device`."""
     torch = _torch()
     if stream is None:
+        if device is not None and device.index is not None:   # without building a Stream object
+            return torch._C._cuda_getCurrentRawStream(device.index)
         stream = torch.cuda.current_stream(device)
     elif device is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _launch(device, stream, cfn, *args):
@@ -175,6 +183,9 @@ def _launch(device, stream, cfn, *args):
     library's device queries and launches address the device that holds the
     tensors; raise on a non-OK status."""
     torch = _torch()
+    if device.index == torch.cuda.current_device():
+        _check(cfn(*args, _stream(stream, device)))
+        return
     with torch.cuda.device(device):
         _check(cfn(*args, _stream(stream, device)))
 
@@ -212,8 +223,15 @@ def _expect(t, shape, dtypes, name, optional=False):
         if optional:
             return
         raise ValueError(f"{name} is required")
-    if t.dim() != len(shape) or any(d is not None and t.shape[i] != d for i, d in enumerate(shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    got = t.shape
+    ok = len(got) == len(shape)
+    if ok:
+        for g, d in zip(got, shape):
+            if d is not None and g != d:
+                ok = False
+                break
+    if not ok:
+        raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
 

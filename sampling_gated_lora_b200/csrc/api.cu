@@ -363,7 +363,7 @@ struct Fp8Layout {
 
 Fp8Layout fp8_layout(int64_t M, int64_t Kc, int64_t No, int32_t r, bool transposed) {
   Fp8Layout l{};
-  l.ld_sx = (M + 127) / 128 * 128;
+  l.ld_sx = (M + 255) / 256 * 256;   // whole token tiles
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;

@@ -36,7 +36,6 @@ struct Fp8Maps {
 struct Fp8Params {
   int M, N, nkb, nkr;        // K-blocks of xq wq^T and of t Bl^T
   int kb_per_split, splits;
-  int stages;
   int ld_sx, ld_sw;          // sx [nkb, ld_sx], sw [ceil(N/128), ld_sw]
   const float* sx;
   const float* sw;
@@ -80,8 +79,8 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
 
 // ---------------------------------------------------------------- few tokens
 // Weights on the 128-row MMA side, BN tokens on the N side: a lane of TMEM is
-// a feature and a column a token. HBM bandwidth bounds these sizes, so W is
-// read once. With fewer tiles than SMs, K is split over a thread-block cluster
+// a feature and a column a token (all of them: M <= BN). HBM bandwidth bounds
+// these sizes, so W is read once. With fewer tiles than SMs, K is split over a thread-block cluster
 // so that every SM streams a share, and the CTAs' fp32 sums meet through
 // distributed shared memory in rank order; otherwise each CTA walks whole
 // tiles, and the stores of one overlap the loads and products of the next.
@@ -93,25 +92,23 @@ struct Narrow {
   static constexpr uint32_t kStage = kWBytes + BN * 128;
   static constexpr int kStride = BN < 32 ? 32 : BN;      // TMEM columns of a buffer
   static constexpr int kBufs = BN <= 64 ? 8 : 512 / BN;
-  static constexpr int kCols = kStride * kBufs;
+  static constexpr int kCols = BN <= 32 ? 256 : 512;
   static constexpr int kEpi = BN <= 64 ? 4 : 8;          // epilogue warps
-  static constexpr int kFirst = BN <= 64 ? 2 : 4;        // the first of them
+  static constexpr int kFirst = 4;                       // the first of them
+  // K-blocks an epilogue warp takes at a time: at few columns the latencies of
+  // a block (barrier, factors, TMEM read) outweigh its adds and would exceed
+  // the 0.36 us in which HBM brings an SM the next 16 KB of W
+  static constexpr int kBatch = BN <= 16 ? 4 : BN <= 64 ? 2 : 1;
+  static constexpr int kStages = 194 * 1024 / static_cast<int>(kStage) < 12 ? 194 * 1024 / static_cast<int>(kStage) : 12;
+  // Scales of a K-block's tokens: copied along with its operands into a ring of
+  // their own. The copies run at most kStages blocks ahead of the MMAs and the
+  // epilogue at most kBufs behind them, so a slot is free when it comes up.
+  static constexpr int kSlots = kStages + kBufs;
+  static_assert(kBufs <= kStages, "the epilogue has to see every phase of a stage's barrier");
   static constexpr int kCW = BN * 4 / kEpi;              // columns of an epilogue warp
   static constexpr int kThreads = 32 * (kFirst + kEpi);
-  static constexpr bool kMoveRegs = BN == 256;           // see kPairThreads
-  // Scales are copied to shared memory kSlots - 1 K-blocks ahead: an L2 read
-  // takes longer than a block of 16 KB of W does at HBM rate (0.36 us an SM).
-  static constexpr int kSlots = BN <= 64 ? 8 : 4;
+  static constexpr bool kMoveRegs = BN > 160;            // see kPairThreads
 };
-
-__device__ __forceinline__ void copy_async4(uint32_t dst, const float* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 template <int BN>
 __global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
@@ -120,13 +117,13 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023u) & ~static_cast<uintptr_t>(1023u));
-  // per epilogue warp: factors of the K-blocks in use, scales (tokens', W's) of those ahead
-  __shared__ alignas(16) float fac[C::kEpi][2][C::kCW];
-  __shared__ float scl[C::kEpi][C::kSlots][C::kCW + 1];
+  __shared__ alignas(16) float fac[C::kEpi][2][C::kBatch][C::kCW];  // per epilogue warp: factors of a batch
+  __shared__ alignas(16) float scl[C::kSlots][BN];
+  __shared__ uint64_t sfull[C::kSlots];
   __shared__ uint64_t acce[C::kBufs];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  const int S = p.stages;
+  constexpr int S = C::kStages;
   // full: a stage has been filled; done: the MMAs on it have completed (frees the
   // stage to the producer and shows the block's sum to the epilogue, which is
   // never more than kBufs <= S blocks behind, so it sees every phase); acce: a
@@ -135,15 +132,15 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
   uint64_t* done = full + S;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tok_tiles = (p.M + BN - 1) / BN;
-  const int tiles = tok_tiles * ((p.N + kRows - 1) / kRows);
+  const int tiles = (p.N + kRows - 1) / kRows;   // one token tile: M <= BN
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&full[s]), 2);   // W's producer and x's
       mbar_init(smem_u32(&done[s]), 1);
     }
     for (int b = 0; b < C::kBufs; ++b) mbar_init(smem_u32(&acce[b]), C::kEpi);
+    for (int b = 0; b < C::kSlots; ++b) mbar_init(smem_u32(&sfull[b]), 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -169,41 +166,45 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
   if (warp < C::kFirst) {
     if (C::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------- TMA producer
-      auto load_w = [&](int tile, int kb, uint32_t st, uint32_t fb) {
-        const int feat0 = tile / tok_tiles * kRows;
-        if (kb < p.nkb) tma_load_2d(st, &tm.w, kb * 128, feat0, fb);
-        else tma_load_2d(st, &tm.b, (kb - p.nkb) * 64, feat0, fb);
-      };
-      auto load_x = [&](int tile, int kb, uint32_t st, uint32_t fb) {
-        const int tok0 = tile % tok_tiles * BN;
-        if (kb < p.nkb) tma_load_2d(st + kWBytes, &tm.x, kb * 128, tok0, fb);
-        else tma_load_2d(st + kWBytes, &tm.t, (kb - p.nkb) * 64, tok0, fb);
-      };
-      // weights (constant) of the first stages before waiting for the writer of xq and t
-      const int pre = min(S, kb1 - kb0);
-      for (int q = 0; q < pre; ++q) {
-        mbar_arrive_expect_tx(smem_u32(&full[q]), C::kStage);
-        load_w(blockIdx.x, kb0 + q, smem_u32(smem + q * C::kStage), smem_u32(&full[q]));
-      }
-      pdl_wait();
-      for (int q = 0; q < pre; ++q)
-        load_x(blockIdx.x, kb0 + q, smem_u32(smem + q * C::kStage), smem_u32(&full[q]));
+      // ---------------------------------------------------------- TMA producer of W (and Bl)
+      // constant, so the first stages do not wait for the writer of xq and t
       Ring st;
-      for (int q = 0; q < pre; ++q) st.next(S);
-      int skip = pre;   // blocks of the first tile that are on their way
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += step, skip = 0)
-        for (int kb = kb0 + skip; kb < kb1; ++kb, st.next(S)) {
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += step)
+        for (int kb = kb0; kb < kb1; ++kb, st.next(S)) {
           if (!mbar_wait(smem_u32(&done[st.i]), st.ph ^ 1u) || abort_flag) {
             fail();
             ok = false;
             break;
           }
           const uint32_t sa = smem_u32(smem + st.i * C::kStage), fb = smem_u32(&full[st.i]);
-          mbar_arrive_expect_tx(fb, C::kStage);
-          load_w(tile, kb, sa, fb);
-          load_x(tile, kb, sa, fb);
+          mbar_arrive_expect_tx(fb, kWBytes);
+          if (kb < p.nkb) tma_load_2d(sa, &tm.w, kb * 128, tile * kRows, fb);
+          else tma_load_2d(sa, &tm.b, (kb - p.nkb) * 64, tile * kRows, fb);
+        }
+    } else if (warp == 2 && lane == 0) {
+      // ---------------------------------------------------------- TMA producer of x (and t) and its scales
+      Ring st, sl;
+      bool ok = true;
+      pdl_wait();
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += step)
+        for (int kb = kb0; kb < kb1; ++kb, st.next(S)) {
+          if (!mbar_wait(smem_u32(&done[st.i]), st.ph ^ 1u) || abort_flag) {
+            fail();
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem_u32(smem + st.i * C::kStage) + kWBytes, fb = smem_u32(&full[st.i]);
+          mbar_arrive_expect_tx(fb, BN * 128);
+          if (kb < p.nkb) {
+            const uint32_t sb = smem_u32(&sfull[sl.i]);
+            tma_load_2d(sa, &tm.x, kb * 128, 0, fb);
+            mbar_arrive_expect_tx(sb, BN * 4);
+            bulk_load(smem_u32(&scl[sl.i]), p.sx + static_cast<size_t>(kb) * p.ld_sx, BN * 4, sb);
+            sl.next(C::kSlots);
+          } else {
+            tma_load_2d(sa, &tm.t, (kb - p.nkb) * 64, 0, fb);
+          }
         }
     } else if (warp == 1 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
@@ -234,84 +235,98 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
   } else {
     // ------------------------------------------------------------ block sums -> registers
     if (C::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    constexpr int kCW = C::kCW, kPer = (kCW + 31) / 32, kChunk = kCW < 32 ? kCW : 32;
+    constexpr int kCW = C::kCW, kPer = (kCW + 31) / 32, kChunk = kCW % 32 ? 16 : 32;
     const int quarter = warp & 3, half = (warp - C::kFirst) >> 2;
     const uint32_t tcol = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kCW);
-    float(*fw)[kCW] = fac[warp - C::kFirst];
+    constexpr int kB = C::kBatch;
+    float(*fw)[kB][kCW] = fac[warp - C::kFirst];
     const int groups = kb1 - kb0;
     pdl_wait();
-    // copy the scales of K-block ahead_g of tile ahead_tile (factor 1 for the adapter's)
-    constexpr int kSlots = C::kSlots;
-    float(*sl)[kCW + 1] = scl[warp - C::kFirst];
-    int ahead_tile = blockIdx.x, ahead_g = 0, ahead = 0;
-    auto prefetch = [&]() {
+    // W's scales: a lane holds one of 32 consecutive K-blocks, the next 32 are on their way
+    int ahead_tile = blockIdx.x, ahead_kb = kb0;
+    auto load_sw = [&]() -> float {
+      float v = 1.f;
       if (ahead_tile < tiles) {
-        float* dst = sl[ahead % kSlots];
-        const int kb = kb0 + ahead_g, t0 = ahead_tile % tok_tiles * BN + half * kCW;
-        const bool main = kb < p.nkb;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int j = lane + 32 * i;
-          if (j < kCW) {
-            if (main && t0 + j < p.ld_sx) copy_async4(smem_u32(dst + j), p.sx + static_cast<size_t>(kb) * p.ld_sx + t0 + j);
-            else dst[j] = 1.f;
-          }
-        }
-        if (lane == 0) {
-          if (main) copy_async4(smem_u32(dst + kCW), p.sw + static_cast<size_t>(ahead_tile / tok_tiles) * p.ld_sw + kb);
-          else dst[kCW] = 1.f;
-        }
-        if (++ahead_g == groups) {
-          ahead_g = 0;
+        if (ahead_kb + lane < min(kb1, p.nkb))
+          v = p.sw[static_cast<size_t>(ahead_tile) * p.ld_sw + ahead_kb + lane];
+        if ((ahead_kb += 32) >= kb1) {
+          ahead_kb = kb0;
           ahead_tile += step;
         }
       }
-      ++ahead;
-      copy_async_commit();
+      return v;
     };
-    for (int i = 0; i < kSlots - 1; ++i) prefetch();
+    float w_now = 1.f, w_next = load_sw();
     int grp = 0;
-    Ring st, buf;
+    Ring st, buf, sl;
     bool ok = true;
     for (int tile = blockIdx.x; ok && tile < tiles; tile += step) {
-      const int tok0 = tile % tok_tiles * BN + half * kCW, feat0 = tile / tok_tiles * kRows;
+      const int tok0 = half * kCW, feat0 = tile * kRows;
       float acc[kCW];
 #pragma unroll
       for (int j = 0; j < kCW; ++j) acc[j] = 0.f;
-      for (int g = 0; g < groups; ++g, ++grp, st.next(S), buf.next(C::kBufs)) {
-        float* f = fw[grp & 1];
-        const float* in = sl[grp % kSlots];
-        copy_async_wait<kSlots - 2>();
-        __syncwarp();
+      for (int g = 0; g < groups; g += kB, ++grp) {
+        float(*f)[kCW] = fw[grp & 1];
+        if ((g & 31) == 0) {
+          w_now = w_next;
+          w_next = load_sw();
+        }
+        // factors of the batch (1 for the adapter's blocks)
+        const int left = min(kB, groups - g);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (lane + 32 * i < kCW) f[lane + 32 * i] = in[lane + 32 * i] * in[kCW];
+        for (int u = 0; u < kB; ++u) {
+          if (u >= left) break;
+          const float ws = __shfl_sync(0xffffffffu, w_now, (g + u) & 31);
+          const bool main = kb0 + g + u < p.nkb;
+          ok = ok && (!main || __all_sync(0xffffffffu, mbar_wait(smem_u32(&sfull[sl.i]), sl.ph)));
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (lane + 32 * i < kCW)
+              f[u][lane + 32 * i] = main ? scl[sl.i][half * kCW + lane + 32 * i] * ws : 1.f;
+          if (main) sl.next(C::kSlots);
+        }
         __syncwarp();
-        prefetch();
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&done[st.i]), st.ph));
+        for (int u = 1; u < left; ++u) st.next(S);   // MMAs complete in order: wait for the batch's last
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&done[st.i]), st.ph));
         if (!ok) break;
+        st.next(S);
         tc_fence_after();
-        const uint32_t t0 = tcol + static_cast<uint32_t>(buf.i * C::kStride);
         uint32_t v[2][kChunk];
-        tmem_ld_async(t0, v[0]);
+        auto col = [&](int q) {   // chunk q of the batch, kCW / kChunk of them to a buffer
+          const int u = q / (kCW / kChunk);
+          int b = buf.i + u;
+          if (b >= C::kBufs) b -= C::kBufs;
+          return tcol + static_cast<uint32_t>(b * C::kStride + q % (kCW / kChunk) * kChunk);
+        };
+        constexpr int kN = kB * (kCW / kChunk);
+        const int nq = left * (kCW / kChunk);
+        tmem_ld_async(col(0), v[0]);
 #pragma unroll
-        for (int c = 0; c < kCW; c += kChunk) {
-          uint32_t(&w)[kChunk] = v[(c / kChunk) & 1];
+        for (int q = 0; q < kN; ++q) {
+          if (q >= nq) break;
+          uint32_t(&w)[kChunk] = v[q & 1];
           tmem_wait_ld(w);
-          if (c + kChunk < kCW) {
-            tmem_ld_async(t0 + c + kChunk, v[(c / kChunk + 1) & 1]);
-          } else {   // the buffer has been read: hand it back to the MMA issuer
+          if (q + 1 < nq) {
+            tmem_ld_async(col(q + 1), v[(q + 1) & 1]);
+          } else {   // the buffers have been read: hand them back to the MMA issuer
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&acce[buf.i]));
+            if (lane < left) {
+              int b = buf.i + lane;
+              if (b >= C::kBufs) b -= C::kBufs;
+              mbar_arrive(smem_u32(&acce[b]));
+            }
           }
+          constexpr int kQ = kCW / kChunk;
+          const int c = q % kQ * kChunk;
 #pragma unroll
           for (int j = 0; j < kChunk; j += 4) {
-            const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(f + c + j);
-            fma2(acc[c + j], acc[c + j + 1], w[j], w[j + 1], q.x);
-            fma2(acc[c + j + 2], acc[c + j + 3], w[j + 2], w[j + 3], q.y);
+            const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(&f[q / kQ][c + j]);
+            fma2(acc[c + j], acc[c + j + 1], w[j], w[j + 1], h.x);
+            fma2(acc[c + j + 2], acc[c + j + 3], w[j + 2], w[j + 3], h.y);
           }
         }
+        for (int u = 0; u < left; ++u) buf.next(C::kBufs);
       }
       if (!ok) break;
       if (p.splits > 1) {
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
     cluster_sync_converged();
     if (!abort_flag) {
       // the CTAs of the cluster share the tile's outputs out, 4 features at a time
-      const int tok0 = static_cast<int>(blockIdx.x) % tok_tiles * BN, feat0 = static_cast<int>(blockIdx.x) / tok_tiles * kRows;
+      const int feat0 = static_cast<int>(blockIdx.x) * kRows;
       constexpr int kGroups = BN * (kRows / 4);
       const int Sp = p.splits;
       const int chunk = (kGroups + Sp - 1) / Sp;
@@ -353,7 +368,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
       for (int r = 0; r < 8; ++r) peer[r] = map_shared_rank(part0, r < Sp ? r : 0);
       for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += C::kThreads) {
         const int j = e / (kRows / 4), i4 = e % (kRows / 4);
-        const int m = tok0 + j, n = feat0 + 4 * i4;
+        const int m = j, n = feat0 + 4 * i4;
         if (m >= p.M || n >= p.N) continue;
         const uint32_t off = static_cast<uint32_t>((j * (kRows + kPartPad) + 4 * i4) * 4);
         float4 v[8];
@@ -386,10 +401,8 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, 1)
 template <int BN>
 uno_status narrow_launch(const Fp8Maps& tm, Fp8Params p, cudaStream_t s) {
   using C = Narrow<BN>;
-  const int64_t tiles = static_cast<int64_t>((p.M + BN - 1) / BN) * ((p.N + kRows - 1) / kRows);
-  if (tiles > (1ll << 30)) return set_error(UNO_ERR_UNSUPPORTED, "too many tiles");
-  p.stages = std::min(12, static_cast<int>(196u * 1024u / C::kStage));
-  const int smem = static_cast<int>(p.stages * (C::kStage + 16) + 1024);
+  const int64_t tiles = (p.N + kRows - 1) / kRows;
+  const int smem = static_cast<int>(C::kStages * (C::kStage + 16) + 1024);
   const int nkb = p.nkb + p.nkr, sms = device_sm_count();
   int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, sms / tiles, nkb})));
   p.kb_per_split = (nkb + splits - 1) / splits;
@@ -651,8 +664,8 @@ uno_status fp8_gemm_launch(const Fp8Gemm& g, cudaStream_t s) {
   p.sw = g.sw;
   p.y = static_cast<__nv_bfloat16*>(g.y);
   p.status = g.status;
-  const bool pair = g.M > 256;
-  const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : g.M <= 128 ? 128 : 256;
+  const bool pair = g.M > 256 || (g.M > 128 && g.N >= 256 * (device_sm_count() / 2));
+  const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : g.M <= 128 ? 128 : g.M <= 160 ? 160 : g.M <= 192 ? 192 : 256;
   const int xbox = pair ? 128 : bn;
   Fp8Maps tm;
   uno_status st;
@@ -670,6 +683,8 @@ uno_status fp8_gemm_launch(const Fp8Gemm& g, cudaStream_t s) {
     case 32: return narrow_launch<32>(tm, p, s);
     case 64: return narrow_launch<64>(tm, p, s);
     case 128: return narrow_launch<128>(tm, p, s);
+    case 160: return narrow_launch<160>(tm, p, s);
+    case 192: return narrow_launch<192>(tm, p, s);
     default: return narrow_launch<256>(tm, p, s);
   }
 }

@@ -277,7 +277,7 @@ struct Fp8Gemm {
   int32_t r;             // 0: no adapter term
   const void* xq;        // [M, K] e4m3
   const float* sx;       // [ceil(K/128), ld_sx]: one scale per row and K-block, K-block major
-  int64_t ld_sx;         // M rounded up to 128
+  int64_t ld_sx;         // M rounded up to 256
   const void* wq;        // [N, K] e4m3
   const float* sw;       // [ceil(N/128), ceil(K/128)]
   const void* t;         // [M, r] bf16, gated and scaled

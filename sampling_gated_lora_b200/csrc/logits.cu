@@ -30,7 +30,7 @@ namespace uno {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 constexpr int kMaxSpecial = kMaxPath + kMaxBias;
 
 // ---------------------------------------------------------------- counts
@@ -120,31 +120,36 @@ __device__ __forceinline__ float apply_rules(const Rules& r, float z, int n, boo
   return z;
 }
 
+// One CTA per segment of a row.
 // kAligned: rows start on 16-byte boundaries (of the logits, the record and,
-// bitwise, the mask). Otherwise a row's 16-byte vectors start at a = row * V
-// mod kN elements before its first id, the first and last are handled id by
-// id, and record words and mask bits are gathered one by one.
+// bitwise, the mask). Otherwise a row's 16-byte vectors start at row * V mod kN
+// elements before its first id, the first and last are handled id by id, and
+// record words and mask bits are gathered one by one.
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kThreads)
-    logits_kernel(const LogitsArgs a, int chunks) {
+__global__ void __launch_bounds__(kThreads, 6)
+    logits_kernel(const LogitsArgs a, int segments, int iters) {
   using Vec = LogitVec<T>;
   constexpr int kN = Vec::kN;
-  constexpr int kChunk = kThreads * kUnroll * kN;
-  __shared__ int32_t ids[kMaxSpecial];
-  __shared__ float vals[kMaxSpecial];
-  const long long row = blockIdx.x / chunks;
-  const int chunk = static_cast<int>(blockIdx.x - row * chunks);
+  constexpr int kStep = kThreads * kUnroll * kN;   // ids of one iteration
+  __shared__ int32_t sp_id[kMaxSpecial];           // special ids in this segment, in any order,
+  __shared__ int32_t sp_src[kMaxSpecial];          // their places in path + bias list,
+  __shared__ float sp_val[kMaxSpecial];            // their biases, then their results
+  __shared__ int sp_n;
+  const long long row = blockIdx.x / segments;
+  const int seg = static_cast<int>(blockIdx.x - row * segments);
   const int b = static_cast<int>(row / a.R), j = static_cast<int>(row - static_cast<long long>(b) * a.R);
   const int V = a.V;
   const T* in = static_cast<const T*>(a.logits) + row * V;
   T* out = static_cast<T*>(a.out) + row * V;
   const int lead = kAligned ? 0 : static_cast<int>((row * V) % kN);
-  const int v_begin = chunk * kChunk - lead;   // id of the chunk's first vector element
+  const int v_begin = seg * iters * kStep - lead;  // id of the segment's first vector element
+  const int v_end = min(V, v_begin + iters * kStep);
+  if (threadIdx.x == 0) sp_n = 0;
   pdl_wait();
 
   const int slot = a.slots ? a.slots[b] : b;
   const bool has_rec = a.counts && slot >= 0 && slot < a.S;
-  if (a.counts && !has_rec && chunk == 0 && threadIdx.x == 0) raise_status(a.dev_status, kDevBadIndex);
+  if (a.counts && !has_rec && seg == 0 && threadIdx.x == 0) raise_status(a.dev_status, kDevBadIndex);
   const unsigned short* rec = has_rec ? a.counts + static_cast<size_t>(slot) * V : nullptr;
   const int mask_words = (V + 31) / 32;
   const uint32_t* mask = a.mask ? a.mask + row * mask_words : nullptr;
@@ -169,125 +174,162 @@ __global__ void __launch_bounds__(kThreads)
     return bits;
   };
   auto whole = [&](int v) { return kAligned ? v < V : v >= 0 && v + kN <= V; };
+  auto vec_id = [&](int it, int u) {
+    return v_begin + ((it * kUnroll + u) * kThreads + static_cast<int>(threadIdx.x)) * kN;
+  };
 
-  // dense loads first: they fly while the special ids are looked up
   uint32_t bits[kUnroll];
-  uint4 z[kUnroll], c[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u)
-    bits[u] = allowed(v_begin + (u * kThreads + static_cast<int>(threadIdx.x)) * kN);
+  for (int u = 0; u < kUnroll; ++u) bits[u] = allowed(vec_id(0, u));
+
+  // ids of the path and of the bias list that fall into this segment; their
+  // results come from the original logits, so before anything is stored
+  const int np = a.path ? (a.path_per_row ? a.P : min(j, a.P)) : 0;
+  const int n_special = np + a.nb;
+  int n_here = 0;
+  if (n_special > 0) {
+    const int32_t* path = a.path + (a.path_per_row ? row : b) * a.P;
+    const size_t bias0 = static_cast<size_t>(b) * a.nb;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_special; i += kThreads) {
+      const int id = i < np ? path[i] : a.bias_ids[bias0 + (i - np)];
+      if (id < 0 || id >= V) {
+        if (id != -1 && seg == 0) raise_status(a.dev_status, kDevBadIndex);
+      } else if (id >= v_begin && id < v_end) {
+        const int k = atomicAdd(&sp_n, 1);
+        sp_id[k] = id;
+        sp_src[k] = i;
+        sp_val[k] = i < np ? 0.f : a.bias[bias0 + (i - np)];
+      }
+    }
+    __syncthreads();
+    n_here = sp_n;
+    if (n_here > 0) {
+      // the first of equal ids acts for all; equal biases add up in list order
+      constexpr int kPer = (kMaxSpecial + kThreads - 1) / kThreads;
+      float res[kPer];
+      uint32_t skip = 0u;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int v = v_begin + (u * kThreads + static_cast<int>(threadIdx.x)) * kN;
-    z[u] = c[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (bits[u] && whole(v)) {
-      z[u] = *reinterpret_cast<const uint4*>(in + v);
-      if (kAligned && rec) {
-        if (kN == 8) {
-          c[u] = *reinterpret_cast<const uint4*>(rec + v);
-        } else {
-          const uint2 h = *reinterpret_cast<const uint2*>(rec + v);
-          c[u].x = h.x;
-          c[u].y = h.y;
+      for (int q = 0; q < kPer; ++q) {
+        const int i = threadIdx.x + q * kThreads;
+        res[q] = 0.f;
+        if (i >= n_here) continue;
+        const int id = sp_id[i], src = sp_src[i];
+        const unsigned short w = rec ? rec[id] : 0;
+        const float z = to_f32<T>(in[id]);
+        const bool on = !mask || ((mask[id >> 5] >> (id & 31)) & 1u);
+        int n = w & 0x7fff, first = src, biases = 0;
+        float add = 0.f;
+        for (int k = 0; k < n_here; ++k)
+          if (sp_id[k] == id) {
+            first = min(first, sp_src[k]);
+            if (sp_src[k] < np) {
+              ++n;
+            } else {
+              ++biases;
+              add = sp_val[k];
+            }
+          }
+        if (biases > 1) {
+          add = 0.f;
+          for (int m = 0, last = np - 1; m < biases; ++m) {
+            int at = -1;
+            for (int k = 0; k < n_here; ++k)
+              if (sp_id[k] == id && sp_src[k] > last && (at < 0 || sp_src[k] < sp_src[at])) at = k;
+            last = sp_src[at];
+            add += sp_val[at];
+          }
+        }
+        float v = apply_rules(r, z, n, n > 0 || (w & 0x8000u));
+        if (biases) v += add;
+        res[q] = on ? v : -INFINITY;
+        if (first != src) skip |= 1u << q;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int i = threadIdx.x + q * kThreads;
+        if (i < n_here) sp_val[i] = res[q];
+        if ((skip >> q) & 1u) sp_id[i] = -1;
+      }
+    }
+  }
+
+  for (int it = 0; it < iters; ++it) {
+    if (vec_id(it, 0) - static_cast<int>(threadIdx.x) * kN >= V) break;   // uniform: the row has ended
+    uint4 z[kUnroll], c[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int v = vec_id(it, u);
+      z[u] = c[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (bits[u] && whole(v)) {
+        z[u] = __ldcs(reinterpret_cast<const uint4*>(in + v));
+        if (kAligned && rec) {
+          if (kN == 8) {
+            c[u] = *reinterpret_cast<const uint4*>(rec + v);
+          } else {
+            const uint2 h = *reinterpret_cast<const uint2*>(rec + v);
+            c[u].x = h.x;
+            c[u].y = h.y;
+          }
         }
       }
     }
-  }
-
-  // ids of the path and of the bias list that fall into this chunk
-  const int np = a.path ? (a.path_per_row ? a.P : min(j, a.P)) : 0;
-  const int n_special = np + a.nb;
-  if (n_special > 0) {
-    const int32_t* path = a.path + (a.path_per_row ? row : b) * a.P;
-    const int32_t* bid = a.bias_ids + static_cast<size_t>(b) * a.nb;
-    for (int i = threadIdx.x; i < n_special; i += kThreads) {
-      int id = i < np ? path[i] : bid[i - np];
-      if (id < 0 || id >= V) {
-        if (id != -1 && chunk == 0) raise_status(a.dev_status, kDevBadIndex);
-        id = -1;
-      }
-      ids[i] = id;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n_special; i += kThreads) {
-      const int id = ids[i];
-      bool mine = id >= 0 && id >= v_begin && id < v_begin + kChunk;
-      for (int q = 0; mine && q < i; ++q) mine = ids[q] != id;   // the first of equal ids acts for all
-      if (!mine) continue;
-      float v = -INFINITY;
-      if (!mask || ((mask[id >> 5] >> (id & 31)) & 1u)) {
-        int n = 0;
-        for (int q = 0; q < np; ++q) n += ids[q] == id;
-        const unsigned short w = rec ? rec[id] : 0;
-        n += w & 0x7fff;
-        v = apply_rules(r, to_f32<T>(in[id]), n, n > 0 || (w & 0x8000u));
-        float add = 0.f;
-        bool any = false;
-        for (int q = np; q < n_special; ++q)
-          if (ids[q] == id) {
-            add += a.bias[static_cast<size_t>(b) * a.nb + (q - np)];
-            any = true;
-          }
-        if (any) v += add;
-      }
-      vals[i] = v;
-    }
-    __syncthreads();
-  }
-
-  // dense results
+    uint32_t now[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int v = v_begin + (u * kThreads + static_cast<int>(threadIdx.x)) * kN;
-    if (whole(v)) {
-      float f[kN];
-      Vec::unpack(z[u], f);
-      if (kAligned) {
-        if (c[u].x | c[u].y | c[u].z | c[u].w) {
-          const uint32_t cw[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+    for (int u = 0; u < kUnroll; ++u) {
+      now[u] = bits[u];
+      if (it + 1 < iters) bits[u] = allowed(vec_id(it + 1, u));
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int v = vec_id(it, u);
+      if (whole(v)) {
+        float f[kN];
+        Vec::unpack(z[u], f);
+        if (kAligned) {
+          if (c[u].x | c[u].y | c[u].z | c[u].w) {
+            const uint32_t cw[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+              const uint32_t w = (cw[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+              f[e] = apply_rules(r, f[e], static_cast<int>(w & 0x7fffu), w != 0);
+            }
+          }
+        } else if (rec && now[u]) {
 #pragma unroll
           for (int e = 0; e < kN; ++e) {
-            const uint32_t w = (cw[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+            const uint32_t w = rec[v + e];
             f[e] = apply_rules(r, f[e], static_cast<int>(w & 0x7fffu), w != 0);
           }
         }
-      } else if (rec && bits[u]) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e)
+          if (!((now[u] >> e) & 1u)) f[e] = -INFINITY;
+        __stcs(reinterpret_cast<uint4*>(out + v), Vec::pack(f));
+      } else if (!kAligned) {
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-          const uint32_t w = rec[v + e];
-          f[e] = apply_rules(r, f[e], static_cast<int>(w & 0x7fffu), w != 0);
+          const int id = v + e;
+          if (id < 0 || id >= V) continue;
+          float f = -INFINITY;
+          if ((now[u] >> e) & 1u) {
+            const uint32_t w = rec ? rec[id] : 0u;
+            f = apply_rules(r, to_f32<T>(in[id]), static_cast<int>(w & 0x7fffu), w != 0);
+          }
+          out[id] = from_f32<T>(f);
         }
-      }
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (!((bits[u] >> e) & 1u)) f[e] = -INFINITY;
-      *reinterpret_cast<uint4*>(out + v) = Vec::pack(f);
-    } else if (!kAligned) {
-#pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        const int id = v + e;
-        if (id < 0 || id >= V) continue;
-        float f = -INFINITY;
-        if ((bits[u] >> e) & 1u) {
-          const uint32_t w = rec ? rec[id] : 0u;
-          f = apply_rules(r, to_f32<T>(in[id]), static_cast<int>(w & 0x7fffu), w != 0);
-        }
-        out[id] = from_f32<T>(f);
       }
     }
   }
-  if (n_special > 0) {
+  if (n_here > 0) {
     __syncthreads();
-    for (int i = threadIdx.x; i < n_special; i += kThreads) {
-      const int id = ids[i];
-      bool mine = id >= 0 && id >= v_begin && id < v_begin + kChunk;
-      for (int q = 0; mine && q < i; ++q) mine = ids[q] != id;
-      if (mine) out[id] = from_f32<T>(vals[i]);
-    }
+    for (int i = threadIdx.x; i < n_here; i += kThreads)
+      if (sp_id[i] >= 0) out[sp_id[i]] = from_f32<T>(sp_val[i]);
   }
 
   // a row whose mask allows nothing is reported (its logits are all -inf)
-  if (mask && chunk == 0) {
+  if (mask && seg == 0) {
     int any = 0;
     for (int w0 = 0; w0 < mask_words && !any; w0 += kThreads) {
       const int w = w0 + static_cast<int>(threadIdx.x);
@@ -302,14 +344,18 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T>
 uno_status logits_dispatch(const LogitsArgs& a, cudaStream_t s) {
   constexpr int kN = LogitVec<T>::kN;
-  constexpr int kChunk = kThreads * kUnroll * kN;
+  constexpr int kStep = kThreads * kUnroll * kN;
   const bool aligned = a.V % 8 == 0;   // 16-byte rows of logits and record, whole bytes of mask
-  const int chunks = aligned ? (a.V + kChunk - 1) / kChunk : (a.V + kN - 1 + kChunk - 1) / kChunk;
-  const int64_t grid = static_cast<int64_t>(a.B) * a.R * chunks;
-  if (grid > 0x7fffffffll) return set_error(UNO_ERR_UNSUPPORTED, "too many logit rows");
-  const dim3 g(static_cast<unsigned>(grid)), t(kThreads);
-  const cudaError_t e = aligned ? launch_kernel(logits_kernel<T, true>, g, t, 0, s, 1, a, chunks)
-                                : launch_kernel(logits_kernel<T, false>, g, t, 0, s, 1, a, chunks);
+  const int steps = (a.V + (aligned ? 0 : kN - 1) + kStep - 1) / kStep;
+  // Long segments spread a CTA's fixed work (parameters, special ids) over more
+  // ids; short ones fill the device when there are few rows.
+  const int64_t rows = static_cast<int64_t>(a.B) * a.R, fill = 12 * device_sm_count();
+  const int iters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, rows * steps / fill)));
+  const int segments = (steps + iters - 1) / iters;
+  if (rows * segments > 0x7fffffffll) return set_error(UNO_ERR_UNSUPPORTED, "too many logit rows");
+  const dim3 g(static_cast<unsigned>(rows * segments)), t(kThreads);
+  const cudaError_t e = aligned ? launch_kernel(logits_kernel<T, true>, g, t, 0, s, 1, a, segments, iters)
+                                : launch_kernel(logits_kernel<T, false>, g, t, 0, s, 1, a, segments, iters);
   return e == cudaSuccess ? UNO_OK : cuda_error(e, "logits rules launch");
 }
 
