@@ -29,8 +29,10 @@ namespace uno {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 2;
+constexpr int kThreads = 256;  // streaming threads
+constexpr int kUnroll = 2;    // 16-byte vectors a thread has in flight
+constexpr int kMaxIters = 8;  // iterations of a segment
+constexpr int kCtas = 5;      // per SM
 constexpr int kMaxSpecial = kMaxPath + kMaxBias;
 
 // ---------------------------------------------------------------- counts
@@ -73,68 +75,101 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- rules
 
+// n: emitted count; held: emitted or in the prompt
+struct Rules {
+  float rho, inv_rho, freq, pres;
+};
+__device__ __forceinline__ float apply_rules(const Rules& r, float z, int n, bool held) {
+  if (held) z *= z > 0.f ? r.inv_rho : r.rho;
+  if (n > 0) z = z - r.freq * static_cast<float>(n) - r.pres;
+  return z;
+}
+__device__ __forceinline__ float apply_rules(const Rules& r, float z, uint32_t word) {
+  return apply_rules(r, z, static_cast<int>(word & 0x7fffu), word != 0u);
+}
+
+// 16 bytes of logits, kept packed. About one id in a hundred has a record, so
+// nearly every warp meets one: only the pairs of ids with a non-zero record
+// word are unpacked and computed (with every id computed, arithmetic instead of
+// HBM was the bound).
 template <typename T>
-struct LogitVec;   // 16 bytes of logits
+struct LogitVec;
 template <>
 struct LogitVec<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void unpack(uint4 w, float (&f)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16_lo(u[i]);
-      f[2 * i + 1] = bf16_hi(u[i]);
-    }
+  static __device__ __forceinline__ uint4 load_record(const unsigned short* p) {
+    return *reinterpret_cast<const uint4*>(p);
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+  static __device__ __forceinline__ uint32_t two(uint32_t z, uint32_t c, const Rules& r) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(apply_rules(r, bf16_lo(z), c & 0xffffu),
+                                                   apply_rules(r, bf16_hi(z), c >> 16));
+    return *reinterpret_cast<const uint32_t*>(&h);   // an id without a record comes back as it was
+  }
+  static __device__ __forceinline__ void rules(uint4& z, const uint4& c, const Rules& r) {
+    if (c.x) z.x = two(z.x, c.x, r);
+    if (c.y) z.y = two(z.y, c.y, r);
+    if (c.z) z.z = two(z.z, c.z, r);
+    if (c.w) z.w = two(z.w, c.w, r);
+  }
+  static __device__ __forceinline__ uint32_t forbid2(uint32_t z, uint32_t bits) {   // two ids, two bits
+    const uint32_t keep = (bits & 1u ? 0xffffu : 0u) | (bits & 2u ? 0xffff0000u : 0u);
+    return (z & keep) | (0xff80ff80u & ~keep);
+  }
+  static __device__ __forceinline__ void forbid(uint4& z, uint32_t bits) {
+    z = make_uint4(forbid2(z.x, bits), forbid2(z.y, bits >> 2), forbid2(z.z, bits >> 4), forbid2(z.w, bits >> 6));
   }
 };
 template <>
 struct LogitVec<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void unpack(uint4 w, float (&f)[4]) {
-    f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
-    f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
+  static __device__ __forceinline__ uint4 load_record(const unsigned short* p) {
+    const uint2 h = *reinterpret_cast<const uint2*>(p);
+    return make_uint4(h.x, h.y, 0u, 0u);
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
+  static __device__ __forceinline__ uint32_t one(uint32_t z, uint32_t w, const Rules& r) {
+    return w ? __float_as_uint(apply_rules(r, __uint_as_float(z), w)) : z;
+  }
+  static __device__ __forceinline__ void rules(uint4& z, const uint4& c, const Rules& r) {
+    if (c.x) {
+      z.x = one(z.x, c.x & 0xffffu, r);
+      z.y = one(z.y, c.x >> 16, r);
+    }
+    if (c.y) {
+      z.z = one(z.z, c.y & 0xffffu, r);
+      z.w = one(z.w, c.y >> 16, r);
+    }
+  }
+  static __device__ __forceinline__ void forbid(uint4& z, uint32_t bits) {
+    const uint32_t inf = 0xff800000u;
+    z = make_uint4(bits & 1u ? z.x : inf, bits & 2u ? z.y : inf, bits & 4u ? z.z : inf, bits & 8u ? z.w : inf);
   }
 };
 
-struct Rules {
-  float rho, freq, pres;
-};
-
-// n: emitted count; held: emitted or in the prompt
-__device__ __forceinline__ float apply_rules(const Rules& r, float z, int n, bool held) {
-  if (held) z = z > 0.f ? __fdiv_rn(z, r.rho) : z * r.rho;
-  if (n > 0) z = z - r.freq * static_cast<float>(n) - r.pres;
-  return z;
-}
-
-// One CTA per segment of a row.
+// One CTA per segment of a row: eight warps stream it, a ninth works out the
+// special ids (path and bias list) meanwhile and overwrites their places when
+// the stream has passed.
 // kAligned: rows start on 16-byte boundaries (of the logits, the record and,
 // bitwise, the mask). Otherwise a row's 16-byte vectors start at row * V mod kN
 // elements before its first id, the first and last are handled id by id, and
 // record words and mask bits are gathered one by one.
+constexpr int kBarRead = 1, kBarStored = 2;   // named barriers of the CTA's nine warps
+
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("barrier.arrive %0, %1;" ::"r"(id), "n"(kThreads + 32) : "memory");
+}
+__device__ __forceinline__ void bar_wait(int id) {
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "n"(kThreads + 32) : "memory");
+}
+
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kThreads, 6)
+__global__ void __launch_bounds__(kThreads + 32, kCtas)
     logits_kernel(const LogitsArgs a, int segments, int iters) {
   using Vec = LogitVec<T>;
   constexpr int kN = Vec::kN;
   constexpr int kStep = kThreads * kUnroll * kN;   // ids of one iteration
-  __shared__ int32_t sp_id[kMaxSpecial];           // special ids in this segment, in any order,
-  __shared__ int32_t sp_src[kMaxSpecial];          // their places in path + bias list,
-  __shared__ float sp_val[kMaxSpecial];            // their biases, then their results
-  __shared__ int sp_n;
+  __shared__ int32_t sp_id[kMaxSpecial];           // special ids in this segment, in list order
+  __shared__ float sp_bias[kMaxSpecial], sp_res[kMaxSpecial];   // their biases and results
+  __shared__ uint32_t seen[kMaxIters * kThreads * kUnroll * 8 / 32];   // ids of the segment met so far
   const long long row = blockIdx.x / segments;
   const int seg = static_cast<int>(blockIdx.x - row * segments);
   const int b = static_cast<int>(row / a.R), j = static_cast<int>(row - static_cast<long long>(b) * a.R);
@@ -144,26 +179,119 @@ __global__ void __launch_bounds__(kThreads, 6)
   const int lead = kAligned ? 0 : static_cast<int>((row * V) % kN);
   const int v_begin = seg * iters * kStep - lead;  // id of the segment's first vector element
   const int v_end = min(V, v_begin + iters * kStep);
-  if (threadIdx.x == 0) sp_n = 0;
+  const int np = a.path ? (a.path_per_row ? a.P : min(j, a.P)) : 0;
+  const int n_special = np + a.nb;
   pdl_wait();
 
   const int slot = a.slots ? a.slots[b] : b;
   const bool has_rec = a.counts && slot >= 0 && slot < a.S;
-  if (a.counts && !has_rec && seg == 0 && threadIdx.x == 0) raise_status(a.dev_status, kDevBadIndex);
   const unsigned short* rec = has_rec ? a.counts + static_cast<size_t>(slot) * V : nullptr;
   const int mask_words = (V + 31) / 32;
   const uint32_t* mask = a.mask ? a.mask + row * mask_words : nullptr;
   Rules r;
   r.rho = a.repetition ? a.repetition[b] : 1.f;
+  r.inv_rho = __fdiv_rn(1.f, r.rho);
   r.freq = a.frequency ? a.frequency[b] : 0.f;
   r.pres = a.presence ? a.presence[b] : 0.f;
 
+  if (threadIdx.x >= kThreads) {
+    // ------------------------------------------------------------ the ninth warp
+    const int lane = threadIdx.x & 31;
+    if (seg == 0) {
+      if (a.counts && !has_rec && lane == 0) raise_status(a.dev_status, kDevBadIndex);
+      if (mask) {   // a row whose mask allows nothing is reported (its logits are all -inf)
+        bool any = false;
+        for (int w0 = 0; w0 < mask_words && !any; w0 += 8 * 32) {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int w = w0 + 32 * q + lane;
+            const uint32_t x = w < mask_words ? mask[w] : 0u;
+            m |= w == mask_words - 1 && (V & 31) ? x & ((1u << (V & 31)) - 1u) : x;
+          }
+          any = __any_sync(0xffffffffu, m != 0u);
+        }
+        if (!any && lane == 0) raise_status(a.dev_status, kDevNoToken);
+      }
+    }
+    if (n_special == 0) return;
+    const int words = (v_end - v_begin + 31) / 32;
+    for (int i = lane; i < words; i += 32) seen[i] = 0u;
+    __syncwarp();
+    const int32_t* path = a.path + (a.path_per_row ? row : b) * a.P;
+    const size_t bias0 = static_cast<size_t>(b) * a.nb;
+    int n = 0, n_path = 0;
+    bool twice = false;   // some id occurs more than once in the list
+    for (int i0 = 0; i0 < n_special; i0 += 32) {
+      const int i = i0 + lane;
+      int id = -1;
+      float bias = 0.f;
+      if (i < np) {
+        id = path[i];
+      } else if (i < n_special) {
+        id = a.bias_ids[bias0 + (i - np)];
+        bias = a.bias[bias0 + (i - np)];
+      }
+      if (id < -1 || id >= V) {
+        if (seg == 0) raise_status(a.dev_status, kDevBadIndex);
+        id = -1;
+      }
+      const bool here = id >= 0 && id >= v_begin && id < v_end;
+      const uint32_t m = __ballot_sync(0xffffffffu, here);
+      if (here) {
+        const int k = n + __popc(m & ((1u << lane) - 1u)), o = id - v_begin;
+        sp_id[k] = id;
+        sp_bias[k] = bias;
+        if (atomicOr(&seen[o >> 5], 1u << (o & 31)) >> (o & 31) & 1u) twice = true;
+      }
+      n_path += __popc(m & __ballot_sync(0xffffffffu, i < np));
+      n += __popc(m);
+    }
+    twice = __any_sync(0xffffffffu, twice);
+    __syncwarp();
+    // results from the original logits, before the stream may store (out may be
+    // logits): the first entry of an id acts for all, biases add up in list order
+    static_assert((kMaxSpecial + 31) / 32 <= 64, "one bit of `acts` a round");
+    uint64_t acts = 0ull;
+    for (int k0 = 0, q = 0; k0 < n; k0 += 32, ++q) {
+      const int k = k0 + lane;
+      if (k < n) {
+        const int id = sp_id[k];
+        const uint32_t w = rec ? rec[id] : 0u;
+        const float z = to_f32<T>(in[id]);
+        const bool on = !mask || ((mask[id >> 5] >> (id & 31)) & 1u);
+        int cnt = static_cast<int>(w & 0x7fffu), first = k;
+        float add = 0.f;
+        if (twice) {
+          for (int e = 0; e < n; ++e)
+            if (sp_id[e] == id) {
+              first = min(first, e);
+              if (e < n_path) ++cnt;
+              else add += sp_bias[e];
+            }
+        } else {
+          cnt += k < n_path;
+          add = sp_bias[k];
+        }
+        if (first == k) acts |= 1ull << q;
+        const float v = apply_rules(r, z, cnt, cnt > 0 || (w & 0x8000u));
+        sp_res[k] = on ? v + add : -INFINITY;
+      }
+    }
+    if (a.logits == a.out) bar_arrive(kBarRead);
+    bar_wait(kBarStored);
+    for (int k = lane, q = 0; k < n; k += 32, ++q)
+      if ((acts >> q) & 1ull) out[sp_id[k]] = from_f32<T>(sp_res[k]);
+    return;
+  }
+
+  // -------------------------------------------------------------- the stream
   // mask bits of the vector's ids (bit e: id v + e); ids outside the row read 0
   auto allowed = [&](int v) -> uint32_t {
     constexpr uint32_t kAll = (1u << kN) - 1u;
     if (kAligned) {
       if (v >= V) return 0u;
-      return mask ? (mask[v >> 5] >> (v & 31)) & kAll : kAll;
+      return mask ? (reinterpret_cast<const uint8_t*>(mask)[v >> 3] >> (v & 7)) & kAll : kAll;
     }
     uint32_t bits = 0u;
 #pragma unroll
@@ -177,136 +305,45 @@ __global__ void __launch_bounds__(kThreads, 6)
   auto vec_id = [&](int it, int u) {
     return v_begin + ((it * kUnroll + u) * kThreads + static_cast<int>(threadIdx.x)) * kN;
   };
-
   uint32_t bits[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) bits[u] = allowed(vec_id(0, u));
 
-  // ids of the path and of the bias list that fall into this segment; their
-  // results come from the original logits, so before anything is stored
-  const int np = a.path ? (a.path_per_row ? a.P : min(j, a.P)) : 0;
-  const int n_special = np + a.nb;
-  int n_here = 0;
-  if (n_special > 0) {
-    const int32_t* path = a.path + (a.path_per_row ? row : b) * a.P;
-    const size_t bias0 = static_cast<size_t>(b) * a.nb;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n_special; i += kThreads) {
-      const int id = i < np ? path[i] : a.bias_ids[bias0 + (i - np)];
-      if (id < 0 || id >= V) {
-        if (id != -1 && seg == 0) raise_status(a.dev_status, kDevBadIndex);
-      } else if (id >= v_begin && id < v_end) {
-        const int k = atomicAdd(&sp_n, 1);
-        sp_id[k] = id;
-        sp_src[k] = i;
-        sp_val[k] = i < np ? 0.f : a.bias[bias0 + (i - np)];
-      }
-    }
-    __syncthreads();
-    n_here = sp_n;
-    if (n_here > 0) {
-      // the first of equal ids acts for all; equal biases add up in list order
-      constexpr int kPer = (kMaxSpecial + kThreads - 1) / kThreads;
-      float res[kPer];
-      uint32_t skip = 0u;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int i = threadIdx.x + q * kThreads;
-        res[q] = 0.f;
-        if (i >= n_here) continue;
-        const int id = sp_id[i], src = sp_src[i];
-        const unsigned short w = rec ? rec[id] : 0;
-        const float z = to_f32<T>(in[id]);
-        const bool on = !mask || ((mask[id >> 5] >> (id & 31)) & 1u);
-        int n = w & 0x7fff, first = src, biases = 0;
-        float add = 0.f;
-        for (int k = 0; k < n_here; ++k)
-          if (sp_id[k] == id) {
-            first = min(first, sp_src[k]);
-            if (sp_src[k] < np) {
-              ++n;
-            } else {
-              ++biases;
-              add = sp_val[k];
-            }
-          }
-        if (biases > 1) {
-          add = 0.f;
-          for (int m = 0, last = np - 1; m < biases; ++m) {
-            int at = -1;
-            for (int k = 0; k < n_here; ++k)
-              if (sp_id[k] == id && sp_src[k] > last && (at < 0 || sp_src[k] < sp_src[at])) at = k;
-            last = sp_src[at];
-            add += sp_val[at];
-          }
-        }
-        float v = apply_rules(r, z, n, n > 0 || (w & 0x8000u));
-        if (biases) v += add;
-        res[q] = on ? v : -INFINITY;
-        if (first != src) skip |= 1u << q;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int i = threadIdx.x + q * kThreads;
-        if (i < n_here) sp_val[i] = res[q];
-        if ((skip >> q) & 1u) sp_id[i] = -1;
-      }
-    }
-  }
-
   for (int it = 0; it < iters; ++it) {
     if (vec_id(it, 0) - static_cast<int>(threadIdx.x) * kN >= V) break;   // uniform: the row has ended
+    // logits and record words (vectors that allow nothing are not read), the
+    // next iteration's mask bits
     uint4 z[kUnroll], c[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int v = vec_id(it, u);
-      z[u] = c[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (bits[u] && whole(v)) {
-        z[u] = __ldcs(reinterpret_cast<const uint4*>(in + v));
-        if (kAligned && rec) {
-          if (kN == 8) {
-            c[u] = *reinterpret_cast<const uint4*>(rec + v);
-          } else {
-            const uint2 h = *reinterpret_cast<const uint2*>(rec + v);
-            c[u].x = h.x;
-            c[u].y = h.y;
-          }
-        }
-      }
-    }
     uint32_t now[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
+      const int v = vec_id(it, u);
       now[u] = bits[u];
-      if (it + 1 < iters) bits[u] = allowed(vec_id(it + 1, u));
+      z[u] = c[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (now[u] && whole(v)) {
+        z[u] = __ldcs(reinterpret_cast<const uint4*>(in + v));
+        if (kAligned && rec) c[u] = Vec::load_record(rec + v);
+      }
     }
+    if (it + 1 < iters) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) bits[u] = allowed(vec_id(it + 1, u));
+    }
+    if (it == 0 && n_special > 0 && a.logits == a.out) bar_wait(kBarRead);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int v = vec_id(it, u);
       if (whole(v)) {
-        float f[kN];
-        Vec::unpack(z[u], f);
         if (kAligned) {
-          if (c[u].x | c[u].y | c[u].z | c[u].w) {
-            const uint32_t cw[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-              const uint32_t w = (cw[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-              f[e] = apply_rules(r, f[e], static_cast<int>(w & 0x7fffu), w != 0);
-            }
-          }
+          if (c[u].x | c[u].y | c[u].z | c[u].w) Vec::rules(z[u], c[u], r);
         } else if (rec && now[u]) {
+          uint32_t w[4] = {};
 #pragma unroll
-          for (int e = 0; e < kN; ++e) {
-            const uint32_t w = rec[v + e];
-            f[e] = apply_rules(r, f[e], static_cast<int>(w & 0x7fffu), w != 0);
-          }
+          for (int e = 0; e < kN; ++e) w[e >> 1] |= static_cast<uint32_t>(rec[v + e]) << (16 * (e & 1));
+          Vec::rules(z[u], make_uint4(w[0], w[1], w[2], w[3]), r);
         }
-#pragma unroll
-        for (int e = 0; e < kN; ++e)
-          if (!((now[u] >> e) & 1u)) f[e] = -INFINITY;
-        __stcs(reinterpret_cast<uint4*>(out + v), Vec::pack(f));
+        if (now[u] != (1u << kN) - 1u) Vec::forbid(z[u], now[u]);
+        __stcs(reinterpret_cast<uint4*>(out + v), z[u]);
       } else if (!kAligned) {
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
@@ -315,30 +352,14 @@ __global__ void __launch_bounds__(kThreads, 6)
           float f = -INFINITY;
           if ((now[u] >> e) & 1u) {
             const uint32_t w = rec ? rec[id] : 0u;
-            f = apply_rules(r, to_f32<T>(in[id]), static_cast<int>(w & 0x7fffu), w != 0);
+            f = apply_rules(r, to_f32<T>(in[id]), w);
           }
           out[id] = from_f32<T>(f);
         }
       }
     }
   }
-  if (n_here > 0) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < n_here; i += kThreads)
-      if (sp_id[i] >= 0) out[sp_id[i]] = from_f32<T>(sp_val[i]);
-  }
-
-  // a row whose mask allows nothing is reported (its logits are all -inf)
-  if (mask && seg == 0) {
-    int any = 0;
-    for (int w0 = 0; w0 < mask_words && !any; w0 += kThreads) {
-      const int w = w0 + static_cast<int>(threadIdx.x);
-      uint32_t m = w < mask_words ? mask[w] : 0u;
-      if (w == mask_words - 1 && (V & 31)) m &= (1u << (V & 31)) - 1u;
-      any = __syncthreads_or(m != 0u);
-    }
-    if (!any && threadIdx.x == 0) raise_status(a.dev_status, kDevNoToken);
-  }
+  if (n_special > 0) bar_arrive(kBarStored);
 }
 
 template <typename T>
@@ -350,10 +371,10 @@ uno_status logits_dispatch(const LogitsArgs& a, cudaStream_t s) {
   // Long segments spread a CTA's fixed work (parameters, special ids) over more
   // ids; short ones fill the device when there are few rows.
   const int64_t rows = static_cast<int64_t>(a.B) * a.R, fill = 12 * device_sm_count();
-  const int iters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, rows * steps / fill)));
+  const int iters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxIters, rows * steps / fill)));
   const int segments = (steps + iters - 1) / iters;
   if (rows * segments > 0x7fffffffll) return set_error(UNO_ERR_UNSUPPORTED, "too many logit rows");
-  const dim3 g(static_cast<unsigned>(rows * segments)), t(kThreads);
+  const dim3 g(static_cast<unsigned>(rows * segments)), t(kThreads + 32);
   const cudaError_t e = aligned ? launch_kernel(logits_kernel<T, true>, g, t, 0, s, 1, a, segments, iters)
                                 : launch_kernel(logits_kernel<T, false>, g, t, 0, s, 1, a, segments, iters);
   return e == cudaSuccess ? UNO_OK : cuda_error(e, "logits rules launch");
