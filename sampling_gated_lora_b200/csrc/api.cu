@@ -402,7 +402,7 @@ uno_status check_fp8(uno_dtype dt, int64_t M, int64_t Kc, int64_t No, int32_t r,
 
 // y [M,No] = x Wq^T (block scales) + scale gate (x A^T) Bl^T; `transposed`: A
 // [r, No] and Bl [Kc, r] come as the forward pass holds them and are transposed
-// here. Launches: (transposes,) quantisation, down-projection, product.
+// here. Launches: (transposes,) quantisation with the down-projection, product.
 uno_status run_fp8(int64_t M, int64_t Kc, int64_t No, int32_t r, const void* x, const void* Wq,
                    const float* Ws, const void* A, const void* Bl, const uint8_t* gate, float scale,
                    void* y, void* workspace, size_t ws_bytes, bool transposed, cudaStream_t st) {
@@ -419,24 +419,32 @@ uno_status run_fp8(int64_t M, int64_t Kc, int64_t No, int32_t r, const void* x, 
   char* base = static_cast<char*>(workspace);
   uno_status s;
   if (transposed && r > 0) {
-    // first, so that the launch that trails the quantisation (which never lets
-    // its dependents start early) may prefetch both as constants
+    // first: the product starts its prologue only when the quantisation has
+    // waited for this launch, and may prefetch the transposes as constants
     if ((s = transpose2_launch(A, r, No, base + L.at, Bl, Kc, r, base + L.blt, st)) != UNO_OK) return s;
     A = base + L.blt;
     Bl = base + L.at;
   }
   float* sx = reinterpret_cast<float*>(base + L.sx);
-  if ((s = fp8_quantize_launch(UNO_BF16, M, Kc, 1, x, reinterpret_cast<uint8_t*>(base + L.xq), sx, 1,
-                               L.ld_sx, st)) != UNO_OK)
-    return s;
   if (r > 0) {
-    const void* As[1] = {A};
-    GemmLaunch down{};
-    if ((s = gemm_prepare(down_problem(UNO_BF16, M, Kc, r, x, As, 1, gate, 0, scale, base + L.t),
-                          &down)) != UNO_OK)
-      return s;
-    if ((s = gemm_run(down, st)) != UNO_OK) return s;
+    Fp8Down d{};
+    d.M = M;
+    d.K = Kc;
+    d.r = r;
+    d.x = x;
+    d.A = A;
+    d.gate = gate;
+    d.scale = scale;
+    d.xq = reinterpret_cast<uint8_t*>(base + L.xq);
+    d.sx = sx;
+    d.ld_sx = L.ld_sx;
+    d.t = base + L.t;
+    s = fp8_down_launch(d, st);
+  } else {
+    s = fp8_quantize_launch(UNO_BF16, M, Kc, 1, x, reinterpret_cast<uint8_t*>(base + L.xq), sx, 1,
+                            L.ld_sx, st);
   }
+  if (s != UNO_OK) return s;
   Fp8Gemm g{};
   g.M = M;
   g.K = Kc;

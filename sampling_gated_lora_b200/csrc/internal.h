@@ -271,6 +271,21 @@ uno_status fp8_quantize_launch(uno_dtype dt, int64_t M, int64_t K, int block_row
                                uint8_t* q, float* scales, int64_t ld_m, int64_t ld_b,
                                cudaStream_t s);
 
+// The same for the rows of x together with t = scale * gate * (x A^T) (fp8_down.cu).
+struct Fp8Down {
+  int64_t M, K;
+  int32_t r;             // >= 8
+  const void* x;         // [M, K] bf16
+  const void* A;         // [r, K] bf16
+  const uint8_t* gate;   // [M]
+  float scale;
+  uint8_t* xq;           // [M, K] e4m3
+  float* sx;             // [ceil(K/128), ld_sx]
+  int64_t ld_sx;
+  void* t;               // [M, r] bf16
+};
+uno_status fp8_down_launch(const Fp8Down& d, cudaStream_t s);
+
 // y [M,N] bf16 = xq wq^T under block scales + t Bl^T (fp8_gemm.cu).
 struct Fp8Gemm {
   int64_t M, K, N;
