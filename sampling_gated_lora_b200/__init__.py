@@ -224,13 +224,8 @@ def _expect(t, shape, dtypes, name, optional=False):
             return
         raise ValueError(f"{name} is required")
     got = t.shape
-    ok = len(got) == len(shape)
-    if ok:
-        for g, d in zip(got, shape):
-            if d is not None and g != d:
-                ok = False
-                break
-    if not ok:
+    if got != shape and (len(got) != len(shape) or
+                         any(d is not None and g != d for g, d in zip(got, shape))):
         raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
@@ -363,11 +358,11 @@ def fp8_quantize(x, block_rows=1, codes=None, scales=None, stream=None):
     _expect(codes, (M, K), (torch.float8_e4m3fn,), "codes", optional=True)
     _expect(scales, shape, (torch.float32,), "scales", optional=True)
     L = load()
-    if codes is None:
-        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
-    if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
     dev = _dev(x, codes, scales)
+    if codes is None:
+        codes = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
+    if scales is None:
+        scales = x.new_empty(shape, dtype=torch.float32)
     _launch(dev, stream, L.uno_fp8_quantize, _dtype(x), M, K, block_rows, _ptr(x), _ptr(codes),
             _ptr(scales))
     return codes, scales
@@ -396,9 +391,9 @@ def gated_lora_linear_fp8(x, Wq, Ws, A, Bl, gate, scale=1.0, y=None, workspace=N
     _expect(gate, (M,), (torch.uint8,), "gate", optional=r == 0)
     _expect(y, (M, N), bf16, "y", optional=True)
     L = load()
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     dev = _dev(x, Wq, Ws, A, Bl, gate, y, workspace)
+    if y is None:
+        y = x.new_empty((M, N))
     ws, wsb = _workspace(L.uno_gated_lora_linear_fp8_workspace(M, K, N, r), dev, workspace)
     _launch(dev, stream, L.uno_gated_lora_linear_fp8, UNO_BF16, M, K, N, r, _ptr(x), _ptr(Wq),
             _ptr(Ws), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(y), _ptr(ws), wsb)
@@ -429,9 +424,9 @@ def gated_lora_input_grad_fp8(dy, Wqt, Wst, A, Bl, gate, scale=1.0, dx=None, wor
     _expect(gate, (M,), (torch.uint8,), "gate", optional=r == 0)
     _expect(dx, (M, K), bf16, "dx", optional=True)
     L = load()
-    if dx is None:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
     dev = _dev(dy, Wqt, Wst, A, Bl, gate, dx, workspace)
+    if dx is None:
+        dx = dy.new_empty((M, K))
     ws, wsb = _workspace(L.uno_gated_lora_input_grad_fp8_workspace(M, K, N, r), dev, workspace)
     _launch(dev, stream, L.uno_gated_lora_input_grad_fp8, UNO_BF16, M, K, N, r, _ptr(dy), _ptr(Wqt),
             _ptr(Wst), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(dx), _ptr(ws), wsb)
@@ -625,9 +620,9 @@ def logits_process(logits, out=None, counts=None, slots=None, draft=None, repeti
     _expect(mask, (B, R, (V + 31) // 32), i32, "mask", optional=True)
     _expect(dev_status, (1,), i32, "dev_status", optional=True)
     L = load()
-    out = torch.empty_like(logits) if out is None else out
     dev = _dev(logits, out, counts, slots, draft, repetition, frequency, presence, bias_ids, bias,
                mask, dev_status)
+    out = torch.empty_like(logits) if out is None else out
     _launch(dev, stream, L.uno_logits_process, _dtype(logits), B, R, V, _ptr(logits), _ptr(out),
             0 if counts is None else counts.shape[0], _ptr(counts), _ptr(slots),
             0 if draft is None else draft.shape[-1], 1 if per_row else 0, _ptr(draft),
