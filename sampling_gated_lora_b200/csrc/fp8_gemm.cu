@@ -29,6 +29,7 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;                           // token rows of a CTA (MMA M, TMEM lanes)
 constexpr int kMaxWidth = 256;                       // features of a tile (MMA N, TMEM columns)
 constexpr int kPartPad = 4;
+constexpr int kPairStages = 6;
 
 struct Fp8Maps {
   CUtensorMap x, w, t, b;
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0;
-  const int S = p.stages;
+  const int S = kPair ? kPairStages : p.stages;
+  const uint32_t x_bytes = kPair ? kRows * 128 : p.x_bytes, stage_bytes = kPair ? 2 * kRows * 128 : p.stage_bytes;
   const int first = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
   const int step = kPair ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
   const int nkb = p.nkb + p.nkr;
@@ -166,19 +168,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         else tma_load_2d(dst, map, c, r, smem_u32(&full[s]));
       };
       auto load_x = [&](int tile, int kb, int s) {
-        const uint32_t dst = smem_u32(smem + s * p.stage_bytes);
+        const uint32_t dst = smem_u32(smem + s * stage_bytes);
         const int m0 = tile % p.tiles_m * kTileRows + static_cast<int>(row0);
         if (kb < p.nkb) load(dst, &tm.x, kb * 128, m0, s);
         else load(dst, &tm.t, (kb - p.nkb) * 64, m0, s);
       };
       auto load_w = [&](int tile, int kb, int s) {
-        const uint32_t dst = smem_u32(smem + s * p.stage_bytes) + p.x_bytes;
+        const uint32_t dst = smem_u32(smem + s * stage_bytes) + x_bytes;
         const int n0 = tile / p.tiles_m * kWidth + static_cast<int>(rank) * (kWidth / 2);
         if (kb < p.nkb) load(dst, &tm.w, kb * 128, n0, s);
         else load(dst, &tm.b, (kb - p.nkb) * 64, n0, s);
       };
       auto expect = [&](int s) {
-        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), (kPair ? 2 : 1) * p.stage_bytes);
+        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), (kPair ? 2 : 1) * stage_bytes);
       };
       // weights (constant) of the first stages before waiting for the writer of xq and t
       Ring st;
@@ -217,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t d = tmem + static_cast<uint32_t>(buf.i * kMaxWidth);
-          const uint32_t sa = smem_u32(smem + st.i * p.stage_bytes);
-          const uint64_t xd = sdesc_k_sw128(sa), wd = sdesc_k_sw128(sa + p.x_bytes);
+          const uint32_t sa = smem_u32(smem + st.i * stage_bytes);
+          const uint64_t xd = sdesc_k_sw128(sa), wd = sdesc_k_sw128(sa + x_bytes);
           if (kb < p.nkb) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -418,35 +420,47 @@ int resident_clusters(int size) {
   return n;
 }
 
-// Tile width and K-split: the fewest K-block passes, a pass over `width`
-// features costing width + kPassCost (the part of a pass that does not shrink
-// with the tile, in features).
-constexpr int kPassCost = 48;
+// The launch form with the least estimated time. A K-block of a tile of w
+// features takes about 350 + 1.2 w ns (measured between 128 and 256 features:
+// the chain from an MMA to its buffer's return, the MMA and the adds), and not
+// less than the 2.8 w ns in which HBM brings its w rows of W to one SM of 148
+// when W passes by once. CTA pairs take the same time for twice the tokens, less
+// 3 % (equal to 7 % faster at 2048 .. 8192 rows); single CTAs fill the device
+// with half the tokens a tile, and can split K.
+struct Plan {
+  bool pair;
+  int width;
+};
 
-// Returns the width.
-int plan(bool pair, Fp8Params* p) {
-  const int rows = pair ? 2 * kRows : kRows, nkb = p->nkb + p->nkr, sms = device_sm_count();
-  p->tiles_m = (p->M + rows - 1) / rows;
-  int64_t best = -1;
-  int width = 0;
-  for (int w : {256, 224, 192, 128}) {
-    if (pair && w < kMaxWidth) break;
-    const int64_t tiles = static_cast<int64_t>(p->tiles_m) * ((p->N + w - 1) / w);
-    const int64_t slots = pair ? std::max(1, sms / 2) : sms;
-    for (int splits = 1; splits <= (pair ? 1 : std::min(8, nkb)); ++splits) {
-      if (splits > 1 && tiles > resident_clusters(splits)) break;   // one wave of clusters only
-      const int per = (nkb + splits - 1) / splits;
-      const int64_t cost = (tiles + slots - 1) / slots * per * (w + kPassCost);
-      if (best < 0 || cost < best) {
-        best = cost;
-        width = w;
-        p->tiles = static_cast<int>(std::min<int64_t>(tiles, 1ll << 30));
-        p->kb_per_split = per;
-        p->splits = (nkb + per - 1) / per;
-      }
+Plan plan(Fp8Params* p) {
+  const int nkb = p->nkb + p->nkr, sms = device_sm_count();
+  Plan best{};
+  double least = -1.;
+  auto consider = [&](bool pair, int w, int splits) {
+    const int rows = pair ? 2 * kRows : kRows, slots = pair ? std::max(1, sms / 2) : sms;
+    const int tiles_m = (p->M + rows - 1) / rows;
+    const int64_t tiles = static_cast<int64_t>(tiles_m) * ((p->N + w - 1) / w);
+    if (splits > 1 && tiles > resident_clusters(splits)) return false;   // one wave of clusters only
+    const int per = (nkb + splits - 1) / splits;
+    double block = 350. + 1.2 * w;
+    if (tiles_m == 1) block = std::max(block, 2.8 * w);
+    if (pair) block *= 0.97;
+    const double cost = static_cast<double>((tiles + slots - 1) / slots) * per * block;
+    if (least < 0. || cost < least) {
+      least = cost;
+      best = Plan{pair, w};
+      p->tiles_m = tiles_m;
+      p->tiles = static_cast<int>(std::min<int64_t>(tiles, 1ll << 30));
+      p->kb_per_split = per;
+      p->splits = (nkb + per - 1) / per;
     }
-  }
-  return width;
+    return true;
+  };
+  for (int w : {256, 224, 192, 128})
+    for (int splits = 1; splits <= std::min(8, nkb) && consider(false, w, splits); ++splits) {
+    }
+  if (p->M > kRows) consider(true, kMaxWidth, 1);
+  return best;
 }
 
 template <bool kPair, int kWidth>
@@ -487,11 +501,10 @@ uno_status fp8_gemm_launch(const Fp8Gemm& g, cudaStream_t s) {
   p.sw = g.sw;
   p.y = static_cast<__nv_bfloat16*>(g.y);
   p.status = g.status;
-  const bool pair = g.M > 256 || (g.M > 128 && g.N >= 256 * (device_sm_count() / 2));
-  const int width = plan(pair, &p);
+  const Plan form = plan(&p);
   if (p.tiles >= (1 << 30)) return set_error(UNO_ERR_UNSUPPORTED, "too many tiles");
-  const int xbox = pair ? kRows : static_cast<int>(std::min<int64_t>(kRows, (g.M + 7) / 8 * 8));
-  const int wbox = pair ? width / 2 : width;
+  const int xbox = form.pair ? kRows : static_cast<int>(std::min<int64_t>(kRows, (g.M + 7) / 8 * 8));
+  const int wbox = form.pair ? form.width / 2 : form.width;
   p.x_bytes = static_cast<uint32_t>(xbox * 128);
   p.stage_bytes = p.x_bytes + static_cast<uint32_t>(wbox * 128);
   Fp8Maps tm;
@@ -504,8 +517,8 @@ uno_status fp8_gemm_launch(const Fp8Gemm& g, cudaStream_t s) {
     if ((st = make_map(&tm.t, UNO_BF16, g.t, g.r, g.M, g.r, xbox)) != UNO_OK) return st;
     if ((st = make_map(&tm.b, UNO_BF16, g.Bl, g.r, g.N, g.r, wbox)) != UNO_OK) return st;
   }
-  if (pair) return gemm_launch<true, 256>(tm, p, s);
-  switch (width) {
+  if (form.pair) return gemm_launch<true, 256>(tm, p, s);
+  switch (form.width) {
     case 256: return gemm_launch<false, 256>(tm, p, s);
     case 224: return gemm_launch<false, 224>(tm, p, s);
     case 192: return gemm_launch<false, 192>(tm, p, s);

@@ -26,7 +26,7 @@ namespace uno {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kBlkThreads = 512;
+constexpr int kBlkThreads = 256;
 
 // 8 consecutive elements as raw words, and as floats.
 template <typename T>
@@ -82,22 +82,20 @@ __device__ __forceinline__ uint2 codes8(const Vec8<T>& v, float inv) {
 // scale of (row m, block b) at scales[m * ld_m + b * ld_b].
 template <typename T, int kIter>
 __global__ void __launch_bounds__(kRowThreads)
-    quantize_rows_kernel(const T* __restrict__ x, long long M, int K, int nkb, uint8_t* __restrict__ q,
+    quantize_rows_kernel(const T* __restrict__ x, uint32_t total, int K, uint32_t nkb, uint8_t* __restrict__ q,
                          float* __restrict__ scales, long long ld_m, long long ld_b) {
-  const long long total = M * nkb;
-  const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const long long first = (static_cast<long long>(blockIdx.x) * kIter) * (kRowThreads / 16) + half;
+  const uint32_t half = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const uint32_t first = blockIdx.x * (kIter * (kRowThreads / 16)) + half;
   pdl_wait();
   Vec8<T> v[kIter];
-  long long off[kIter];
+  size_t off[kIter];
   bool in[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const long long b = first + static_cast<long long>(i) * (kRowThreads / 16);
-    const long long m = b / nkb;
-    const int kb = static_cast<int>(b - m * nkb), c = kb * 128 + l * 8;
+    const uint32_t b = first + i * (kRowThreads / 16), m = b / nkb;
+    const int c = static_cast<int>((b - m * nkb) * 128 + l * 8);
     in[i] = b < total && c < K;
-    off[i] = m * K + c;
+    off[i] = static_cast<size_t>(m) * K + c;
     if (in[i]) v[i].load(x + off[i]);
     else v[i].zero();
   }
@@ -108,16 +106,16 @@ __global__ void __launch_bounds__(kRowThreads)
     for (int o = 8; o; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
     a = max_nan(a, kAmaxFloor);
     if (in[i]) *reinterpret_cast<uint2*>(q + off[i]) = codes8(v[i], __fdiv_rn(kE4m3Max, a));
-    const long long b = first + static_cast<long long>(i) * (kRowThreads / 16);
+    const uint32_t b = first + i * (kRowThreads / 16);
     if (l == 0 && b < total) {
-      const long long m = b / nkb;
+      const uint32_t m = b / nkb;
       scales[m * ld_m + (b - m * nkb) * ld_b] = __fdiv_rn(a, kE4m3Max);
     }
   }
 }
 
 // 128 x 128 blocks: one CTA each, the block in registers between the maximum
-// and the conversion (4 vectors a thread).
+// and the conversion (8 vectors a thread).
 template <typename T>
 __global__ void __launch_bounds__(kBlkThreads)
     quantize_blocks_kernel(const T* __restrict__ x, long long M, int K, int nkb, uint8_t* __restrict__ q,
@@ -162,15 +160,14 @@ uno_status rows_launch(const T* x, int64_t M, int64_t K, uint8_t* q, float* scal
   // one block per half warp until the grid fills the device, then four in flight
   const bool wide = blocks >= static_cast<int64_t>(device_sm_count()) * per * 16;
   const int64_t grid = (blocks + per * (wide ? 4 : 1) - 1) / (per * (wide ? 4 : 1));
-  if (grid > 0x7fffffffll) return set_error(UNO_ERR_UNSUPPORTED, "too many blocks to quantise");
+  if (blocks > 0x7fffffffll) return set_error(UNO_ERR_UNSUPPORTED, "too many blocks to quantise");
   const dim3 g(static_cast<unsigned>(grid)), b(kRowThreads);
+  const uint32_t total = static_cast<uint32_t>(blocks), per_row = static_cast<uint32_t>(nkb);
+  const long long lm = ld_m, lb = ld_b;
+  const int k = static_cast<int>(K);
   const cudaError_t e =
-      wide ? launch_kernel(quantize_rows_kernel<T, 4>, g, b, 0, s, 1, x, static_cast<long long>(M),
-                           static_cast<int>(K), nkb, q, scales, static_cast<long long>(ld_m),
-                           static_cast<long long>(ld_b))
-           : launch_kernel(quantize_rows_kernel<T, 1>, g, b, 0, s, 1, x, static_cast<long long>(M),
-                           static_cast<int>(K), nkb, q, scales, static_cast<long long>(ld_m),
-                           static_cast<long long>(ld_b));
+      wide ? launch_kernel(quantize_rows_kernel<T, 4>, g, b, 0, s, 1, x, total, k, per_row, q, scales, lm, lb)
+           : launch_kernel(quantize_rows_kernel<T, 1>, g, b, 0, s, 1, x, total, k, per_row, q, scales, lm, lb);
   return e == cudaSuccess ? UNO_OK : cuda_error(e, "row quantisation launch");
 }
 
