@@ -53,7 +53,7 @@ typedef enum { UNO_BF16 = 0, UNO_F32 = 1 } uno_dtype;
 
 /* Device status bits (dev_status words and uno_device_status). */
 #define UNO_DEV_BAD_DRAFT 1 /* a draft id outside [0, V): that sequence's outputs are -1 */
-#define UNO_DEV_NAN 2       /* a NaN logit in a row that was read: outputs are -1 */
+#define UNO_DEV_NAN 2       /* a NaN logit (or no finite one) in a row that was read: outputs are -1 */
 #define UNO_DEV_TIMEOUT 4   /* a bounded on-device wait gave up (kernel returned early) */
 #define UNO_DEV_BAD_INDEX 8 /* a token id or a slot outside its range: that entry was skipped */
 #define UNO_DEV_NO_TOKEN 16 /* a logits row whose mask allows no token: its logits are all -inf */
@@ -222,7 +222,9 @@ uno_status uno_gated_lora_input_grad_fp8(uno_dtype dt, int64_t M, int64_t K, int
  *                 itself if that sum is 0);
  *       if n = k and k_p = k+1: the bonus, same rule on p_k with u3;
  *     padded with -1; out_count[b] = number of tokens written.
- *   out_tokens is [B, k+1]. T > 0. 1 <= k <= 32, 2 <= V <= 196608.
+ *   out_tokens is [B, k+1]. T > 0. 1 <= k <= 32, 2 <= V <= 196608. Logits of
+ *   -inf have probability 0 (masked ids); a row of nothing but -inf is reported
+ *   like one with a NaN.
  *   dev_status: optional int32 device word, OR-ed with UNO_DEV_* bits.
  * ------------------------------------------------------------------------- */
 size_t uno_psi_verify_workspace(int32_t B, int32_t k, int32_t k_p, int32_t V);
@@ -403,8 +405,8 @@ uno_status uno_draft_sample(uno_dtype dt, int32_t B, int32_t k, int32_t V, const
                             size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Rules on logits, applied before drafting, verification or distillation (a
- * library addition: sampling from a distribution the user has penalised,
+ * Rules on logits, applied before drafting or verification (a library
+ * addition: sampling from a distribution the user has penalised,
  * biased or masked stays lossless with respect to that distribution when the
  * AR rows get the rules of their own prefixes).
  *

@@ -97,7 +97,9 @@ struct OnlineStat {
       s *= fast_exp2((m - mx) * c);
       m = mx;
     }
-    for (int e = 0; e < n; ++e) s += fast_exp2((v[e] - m) * c);
+    // while only -inf has been seen the weights are 0 (and a NaN still shows)
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int e = 0; e < n; ++e) s += fast_exp2((v[e] - ref) * c);
   }
 };
 
@@ -475,7 +477,8 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
   }
 }
 
-// Merge the chunk stats of one row.
+// Merge the chunk stats of one row. A row without a finite logit has no
+// distribution: its sum is NaN, as with a NaN logit.
 __device__ __forceinline__ float2 row_stat(const float2* stats, int row, int chunks, float c) {
   float m = -INFINITY, s = 0.f;
   bool nan = false;
@@ -484,7 +487,7 @@ __device__ __forceinline__ float2 row_stat(const float2* stats, int row, int chu
     nan |= isnan(v.y);
     merge_stat(m, s, v.x, v.y, c);
   }
-  return make_float2(m, nan ? NAN : s);
+  return make_float2(m, nan || m == -INFINITY ? NAN : s);
 }
 
 // ------------------------------------------------------------------ cluster inverse-CDF draw
@@ -1779,7 +1782,7 @@ __device__ __forceinline__ float3 vp_merge(const float4* parts, int rows, int ro
     merge_stat(m, s, v.x, v.y, c);
     z = fmaxf(z, v.z);
   }
-  return make_float3(m, nan ? NAN : s, z);
+  return make_float3(m, nan || m == -INFINITY ? NAN : s, z);   // as row_stat
 }
 
 // One warp per sequence: lane j tests position j (as verify_finalize).
