@@ -13,6 +13,12 @@ from gpu_util import dev_tensor, host_f64
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def _clean_status():
+    import sampling_gated_lora_b200 as U
+    U.device_status(clear=True)   # the word is the library's: other tests leave bits in it
+
+
 def _codes(t):
     import torch
     return t.view(torch.uint8).cpu().numpy()
@@ -94,6 +100,8 @@ SHAPES = [
     (17, 2048, 200, 24), (32, 272, 1000, 256), (33, 1040, 1000, 24), (64, 4096, 384, 128), (65, 640, 256, 8),
     (128, 1024, 1024, 128), (129, 528, 264, 40), (200, 12288, 136, 128), (257, 1024, 520, 16), (300, 144, 2048, 200),
     (577, 1040, 776, 128), (1000, 512, 4096, 128),
+    (40, 128, 40064, 256), (300, 128, 20480, 256), (129, 1024, 37888, 8), (5000, 144, 264, 16),   # several tiles a CTA
+    (100, 256, 33024, 0), (2500, 272, 2304, 128),
 ]
 
 
@@ -128,6 +136,39 @@ def test_input_gradient_matches_the_oracle(M, K, N, r):
     f = lambda z: None if z is None else W.bf16_to_f64(z)   # noqa: E731
     _near(dx, *fp8.gated_input_grad_fp8(f(dy), fp8.code_values()[codes], Ws, f(A), f(Bl), gate, 0.5),
           f"{M}x{K}x{N} r={r}")
+
+
+def test_gradient_is_what_differences_of_the_output_say():
+    """Row by row, <dy, y(x + d) - y(x)> = <dx, d>. x and dy hold exact e4m3 values with a 448 in every block
+    (scales 1), and d turns those around, so x and x + d are exact too. What rounds is bf16: y twice, t = x A^T
+    twice, u = dy Bl and dx once, each by 2^-8 of its values; 2^-14 covers the fp32 sums (128-deep blocks)."""
+    import torch
+    import sampling_gated_lora_b200 as U
+    M, K, N, r = 24, 256, 384, 16
+    rng = np.random.default_rng(4)
+    _, codes, Ws, A, Bl, gate = _case(M, K, N, r, seed=4)
+    gate[:] = 1
+
+    def draw(*shape):
+        v = rng.choice(np.array([-4.0, -2.0, -1.0, 0.0, 1.0, 2.0, 4.0]), shape)
+        v[:, ::128] = 448.0
+        return v
+    x0, dy = draw(M, K), draw(M, N)
+    d = np.zeros((M, K))
+    d[:, ::128] = -896.0
+    args = _dev(W.bf16_round(x0), codes, Ws, A, Bl, gate)
+    wqt = args[1].view(torch.uint8).t().contiguous().view(torch.float8_e4m3fn)
+    t = lambda v: dev_tensor(W.bf16_round(v), "bf16")   # noqa: E731
+    dx = host_f64(U.gated_lora_input_grad_fp8(t(dy), wqt, args[2].t().contiguous(), *args[3:], 0.5))
+    y0, y1 = (host_f64(U.gated_lora_linear_fp8(t(v), *args[1:], 0.5)) for v in (x0, x0 + d))
+    a, b = W.bf16_to_f64(A), W.bf16_to_f64(Bl)
+    ts = sum(np.abs(0.5 * v @ a.T) for v in (x0, x0 + d)) @ np.abs(b).T     # |t| through the up-projection
+    us = np.abs(0.5 * dy @ b) @ np.abs(a)                                     # |u| through A
+    ay = np.abs(y0) + np.abs(y1)
+    tol = (2.0 ** -8 + 2.0 ** -14) * ((np.abs(dy) * (ay + ts)).sum(1) + (np.abs(d) * (np.abs(dx) + us)).sum(1))
+    moved, said = (dy * (y1 - y0)).sum(1), (dx * d).sum(1)
+    assert np.all(np.abs(moved - said) <= tol)
+    assert np.median(np.abs(said) / tol) > 2     # the test can tell
 
 
 def test_gate_zero_rows_are_the_base_product_and_no_rows_launch_nothing():
