@@ -85,9 +85,11 @@ struct Vec<float> {
   }
 };
 
-// Online (max, sum of exp2((z - max) * c)) of one thread.
+// Online (max, sum of exp2((z - max) * c)) of one thread. The max starts at the
+// lowest finite float, so that -inf logits (masked ids) weigh 0 from the first
+// one on; s = 0 tells that nothing finite was seen.
 struct OnlineStat {
-  float m = -INFINITY;
+  float m = -FLT_MAX;
   float s = 0.f;
   template <typename C>
   __device__ __forceinline__ void add(const float* v, int n, C c) {
@@ -97,9 +99,7 @@ struct OnlineStat {
       s *= fast_exp2((m - mx) * c);
       m = mx;
     }
-    // while only -inf has been seen the weights are 0 (and a NaN still shows)
-    const float ref = m == -INFINITY ? 0.f : m;
-    for (int e = 0; e < n; ++e) s += fast_exp2((v[e] - ref) * c);
+    for (int e = 0; e < n; ++e) s += fast_exp2((v[e] - m) * c);
   }
 };
 
@@ -174,7 +174,7 @@ __device__ __forceinline__ float2 block_row_stat(const T* z, int lo, int hi, C c
   float M = sm[0], S = ss[0];
   if (threadIdx.x == 0)
     for (int w = 1; w < kStatThreads / 32; ++w) merge_stat(M, S, sm[w], ss[w], c);
-  return make_float2(M, S);
+  return make_float2(S == 0.f ? -INFINITY : M, S);
 }
 
 // Grid: rows * chunks blocks, one per (row, vocab chunk), chunk fastest (a
