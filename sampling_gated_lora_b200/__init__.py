@@ -21,6 +21,7 @@ Functions mirror the C ABI:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -236,13 +237,23 @@ def _floats():
     return (torch.bfloat16, torch.float32)
 
 
-def _workspace(nbytes, device, workspace):
+def _workspace(nbytes, device, workspace, stream=None):
     torch = _torch()
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with _allocating_on(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return workspace, workspace.numel() * workspace.element_size()
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _allocating_on(stream):
+    """Context in which torch allocates for work on `stream` (None: the current stream): memory
+    from another stream's pool could still be in use there, or be handed out again too early."""
+    return _NO_CONTEXT if stream is None else _torch().cuda.stream(stream)
 
 
 # ---------------------------------------------------------------- operations
@@ -359,10 +370,11 @@ def fp8_quantize(x, block_rows=1, codes=None, scales=None, stream=None):
     _expect(scales, shape, (torch.float32,), "scales", optional=True)
     L = load()
     dev = _dev(x, codes, scales)
-    if codes is None:
-        codes = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
-    if scales is None:
-        scales = x.new_empty(shape, dtype=torch.float32)
+    with _allocating_on(stream):
+        if codes is None:
+            codes = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
+        if scales is None:
+            scales = x.new_empty(shape, dtype=torch.float32)
     _launch(dev, stream, L.uno_fp8_quantize, _dtype(x), M, K, block_rows, _ptr(x), _ptr(codes),
             _ptr(scales))
     return codes, scales
@@ -393,8 +405,9 @@ def gated_lora_linear_fp8(x, Wq, Ws, A, Bl, gate, scale=1.0, y=None, workspace=N
     L = load()
     dev = _dev(x, Wq, Ws, A, Bl, gate, y, workspace)
     if y is None:
-        y = x.new_empty((M, N))
-    ws, wsb = _workspace(L.uno_gated_lora_linear_fp8_workspace(M, K, N, r), dev, workspace)
+        with _allocating_on(stream):
+            y = x.new_empty((M, N))
+    ws, wsb = _workspace(L.uno_gated_lora_linear_fp8_workspace(M, K, N, r), dev, workspace, stream)
     _launch(dev, stream, L.uno_gated_lora_linear_fp8, UNO_BF16, M, K, N, r, _ptr(x), _ptr(Wq),
             _ptr(Ws), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(y), _ptr(ws), wsb)
     return y
@@ -426,8 +439,9 @@ def gated_lora_input_grad_fp8(dy, Wqt, Wst, A, Bl, gate, scale=1.0, dx=None, wor
     L = load()
     dev = _dev(dy, Wqt, Wst, A, Bl, gate, dx, workspace)
     if dx is None:
-        dx = dy.new_empty((M, K))
-    ws, wsb = _workspace(L.uno_gated_lora_input_grad_fp8_workspace(M, K, N, r), dev, workspace)
+        with _allocating_on(stream):
+            dx = dy.new_empty((M, K))
+    ws, wsb = _workspace(L.uno_gated_lora_input_grad_fp8_workspace(M, K, N, r), dev, workspace, stream)
     _launch(dev, stream, L.uno_gated_lora_input_grad_fp8, UNO_BF16, M, K, N, r, _ptr(dy), _ptr(Wqt),
             _ptr(Wst), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(dx), _ptr(ws), wsb)
     return dx
@@ -622,7 +636,9 @@ def logits_process(logits, out=None, counts=None, slots=None, draft=None, repeti
     L = load()
     dev = _dev(logits, out, counts, slots, draft, repetition, frequency, presence, bias_ids, bias,
                mask, dev_status)
-    out = torch.empty_like(logits) if out is None else out
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty_like(logits)
     _launch(dev, stream, L.uno_logits_process, _dtype(logits), B, R, V, _ptr(logits), _ptr(out),
             0 if counts is None else counts.shape[0], _ptr(counts), _ptr(slots),
             0 if draft is None else draft.shape[-1], 1 if per_row else 0, _ptr(draft),

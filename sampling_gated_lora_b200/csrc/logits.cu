@@ -162,7 +162,7 @@ __device__ __forceinline__ void bar_wait(int id) {
 }
 
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kThreads + 32, kCtas)
+__global__ void __launch_bounds__(kThreads + 32, kAligned ? kCtas : kCtas - 1)
     logits_kernel(const LogitsArgs a, int segments, int iters) {
   using Vec = LogitVec<T>;
   constexpr int kN = Vec::kN;
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas)
   const int np = a.path ? (a.path_per_row ? a.P : min(j, a.P)) : 0;
   const int n_special = np + a.nb;
   pdl_wait();
+  if (v_begin >= V) return;   // an unaligned row that ends before its last segment
 
   const int slot = a.slots ? a.slots[b] : b;
   const bool has_rec = a.counts && slot >= 0 && slot < a.S;

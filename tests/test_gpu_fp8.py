@@ -96,7 +96,7 @@ def _near(y, ref, bound, what):
 
 
 SHAPES = [
-    (1, 16, 8, 0), (1, 128, 128, 8), (2, 144, 136, 16), (9, 1024, 512, 128), (16, 512, 4096, 64),
+    (1, 16, 8, 0), (1, 128, 128, 8), (5, 16, 16, 8), (150, 16, 8, 200), (2, 144, 136, 16), (9, 1024, 512, 128), (16, 512, 4096, 64),
     (17, 2048, 200, 24), (32, 272, 1000, 256), (33, 1040, 1000, 24), (64, 4096, 384, 128), (65, 640, 256, 8),
     (128, 1024, 1024, 128), (129, 528, 264, 40), (200, 12288, 136, 128), (257, 1024, 520, 16), (300, 144, 2048, 200),
     (577, 1040, 776, 128), (1000, 512, 4096, 128),
@@ -227,3 +227,48 @@ def test_graph_replays_streams_and_a_shared_workspace(M):
             assert torch.equal(got, want if k != 1 else -want)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.all(big[0] == 7.0) and torch.all(big[-1] == 7.0)
+
+
+def test_calls_on_a_stream_given_by_argument():
+    """Outputs and workspaces made by the call belong to that stream: two of them run their calls side by side."""
+    import torch
+    import sampling_gated_lora_b200 as U
+    cases = [_dev(*_case(M, 512, 384, 16, seed=M)) for M in (20, 200)]
+    want = [U.gated_lora_linear_fp8(*c, 0.75) for c in cases]
+    codes = U.fp8_quantize(cases[1][0])[0]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(U.gated_lora_linear_fp8(*cases[i], 0.75, stream=s))
+            other = U.fp8_quantize(cases[1][0], stream=s)[0]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for ys, w in zip(got, want) for y in ys)
+    assert torch.equal(other.view(torch.uint8), codes.view(torch.uint8))
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, sampling_gated_lora_b200 as U
+g = torch.Generator(device="cuda").manual_seed(0)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+x, A, Bl, gate = r(9, 256), r(8, 256), r(384, 8), torch.ones(9, dtype=torch.uint8, device="cuda")
+Wq = (torch.randn(384, 256, generator=g, device="cuda")).to(torch.float8_e4m3fn)
+Ws = torch.full((3, 2), 0.5, device="cuda")
+z, y = r(1, 2, 1000), torch.zeros(9, 384, device="cuda", dtype=torch.bfloat16)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    U.gated_lora_linear_fp8(x, Wq, Ws, A, Bl, gate, 1.0, y=y)
+    U.logits_process(z, out=z, presence=torch.ones(1, device="cuda"))
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, U.gated_lora_linear_fp8(x, Wq, Ws, A, Bl, gate, 1.0)) and bool(y.any())
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=300)
