@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -225,9 +226,14 @@ def _expect(t, shape, dtypes, name, optional=False):
             return
         raise ValueError(f"{name} is required")
     got = t.shape
-    if got != shape and (len(got) != len(shape) or
-                         any(d is not None and g != d for g, d in zip(got, shape))):
-        raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
+    if got != shape:
+        ok = len(got) == len(shape)
+        if ok:
+            for g, d in zip(got, shape):
+                if g != d and d is not None:
+                    ok = False
+        if not ok:
+            raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
 
@@ -244,16 +250,21 @@ def _workspace(nbytes, device, workspace, stream=None):
     if workspace is None:
         with _allocating_on(stream):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return workspace, workspace.numel() * workspace.element_size()
-
-
-_NO_CONTEXT = contextlib.nullcontext()
+    return workspace, workspace.nbytes
 
 
 def _allocating_on(stream):
     """Context in which torch allocates for work on `stream` (None: the current stream): memory
     from another stream's pool could still be in use there, or be handed out again too early."""
-    return _NO_CONTEXT if stream is None else _torch().cuda.stream(stream)
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _new(like, shape, dtype, stream):
+    """An uninitialised tensor on like's device for work on `stream`."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _allocating_on(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 # ---------------------------------------------------------------- operations
@@ -370,16 +381,16 @@ def fp8_quantize(x, block_rows=1, codes=None, scales=None, stream=None):
     _expect(scales, shape, (torch.float32,), "scales", optional=True)
     L = load()
     dev = _dev(x, codes, scales)
-    with _allocating_on(stream):
-        if codes is None:
-            codes = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
-        if scales is None:
-            scales = x.new_empty(shape, dtype=torch.float32)
+    if codes is None:
+        codes = _new(x, (M, K), torch.float8_e4m3fn, stream)
+    if scales is None:
+        scales = _new(x, shape, torch.float32, stream)
     _launch(dev, stream, L.uno_fp8_quantize, _dtype(x), M, K, block_rows, _ptr(x), _ptr(codes),
             _ptr(scales))
     return codes, scales
 
 
+@functools.lru_cache(maxsize=4096)
 def gated_lora_linear_fp8_workspace(M, K, N, r):
     """Bytes of the workspace of gated_lora_linear_fp8."""
     return load().uno_gated_lora_linear_fp8_workspace(M, K, N, r)
@@ -405,14 +416,14 @@ def gated_lora_linear_fp8(x, Wq, Ws, A, Bl, gate, scale=1.0, y=None, workspace=N
     L = load()
     dev = _dev(x, Wq, Ws, A, Bl, gate, y, workspace)
     if y is None:
-        with _allocating_on(stream):
-            y = x.new_empty((M, N))
-    ws, wsb = _workspace(L.uno_gated_lora_linear_fp8_workspace(M, K, N, r), dev, workspace, stream)
+        y = _new(x, (M, N), x.dtype, stream)
+    ws, wsb = _workspace(gated_lora_linear_fp8_workspace(M, K, N, r), dev, workspace, stream)
     _launch(dev, stream, L.uno_gated_lora_linear_fp8, UNO_BF16, M, K, N, r, _ptr(x), _ptr(Wq),
             _ptr(Ws), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(y), _ptr(ws), wsb)
     return y
 
 
+@functools.lru_cache(maxsize=4096)
 def gated_lora_input_grad_fp8_workspace(M, K, N, r):
     """Bytes of the workspace of gated_lora_input_grad_fp8."""
     return load().uno_gated_lora_input_grad_fp8_workspace(M, K, N, r)
@@ -439,9 +450,8 @@ def gated_lora_input_grad_fp8(dy, Wqt, Wst, A, Bl, gate, scale=1.0, dx=None, wor
     L = load()
     dev = _dev(dy, Wqt, Wst, A, Bl, gate, dx, workspace)
     if dx is None:
-        with _allocating_on(stream):
-            dx = dy.new_empty((M, K))
-    ws, wsb = _workspace(L.uno_gated_lora_input_grad_fp8_workspace(M, K, N, r), dev, workspace, stream)
+        dx = _new(dy, (M, K), dy.dtype, stream)
+    ws, wsb = _workspace(gated_lora_input_grad_fp8_workspace(M, K, N, r), dev, workspace, stream)
     _launch(dev, stream, L.uno_gated_lora_input_grad_fp8, UNO_BF16, M, K, N, r, _ptr(dy), _ptr(Wqt),
             _ptr(Wst), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(dx), _ptr(ws), wsb)
     return dx
