@@ -5,11 +5,13 @@
 //   t       scale * gate(m) * (x A^T) [M,r] in bf16: the gated adapter's
 //           down-projection (hyper.ai, section "方法"), from x itself
 //
-// x arrives by TMA once; a tensor-core pass takes it as one operand of A x^T
-// (adapter rows on the 128-row side, BT tokens on the other, fp32 in TMEM)
+// x arrives by TMA; a tensor-core pass takes a tile of BT tokens as one operand
+// of x A^T (tokens on the 128-row side, adapter rows on the other, fp32 in TMEM)
 // while eight warps read the same tile from shared memory, find each row's
 // maximum over the block and write its codes. K is split over a thread-block
 // cluster; the CTAs' T meet through distributed shared memory in rank order.
+// With few tokens A is most of what is read, and chunks of 32 adapter rows go
+// to clusters of their own (the first of them quantises).
 // HBM bounds it for many rows (3 bytes an element; two separate passes over x
 // measured 43 + 25 us at 4352 x 12288), latency for few.
 #include <algorithm>
@@ -24,9 +26,8 @@ namespace uno {
 namespace {
 
 constexpr int kThreads = 320;         // producer, MMA issuer, eight quantising warps
-constexpr int kRows = 128;            // adapter rows of an A tile
+constexpr int kLanes = 128;           // MMA M: token rows, whatever part of them a tile has
 constexpr int kPartPad = 4;
-constexpr uint32_t kABytes = kRows * 256;   // 128 adapter rows x 128 k: two 64-wide boxes
 
 struct DownMaps {
   CUtensorMap x, a;
@@ -41,21 +42,24 @@ struct DownParams {
   __nv_bfloat16* t;
 };
 
-// NA: A tiles of 128 adapter rows (r <= 256)
-template <int BT, int NA>
+// A CTA's tile: BT tokens, NA boxes of RC adapter rows.
+template <int BT, int RC, int NA>
 struct Down {
-  static constexpr uint32_t kX = BT * 256;
-  static constexpr uint32_t kStage = kX + NA * kABytes;
-  static constexpr int kFit = 192 * 1024 / static_cast<int>(kStage);
-  static constexpr int kStages = kFit < 6 ? kFit : 6;
-  static constexpr int kCols = NA * BT < 32 ? 32 : NA * BT;
-  static_assert(NA * BT * (kRows + kPartPad) * 4 <= kStages * static_cast<int>(kStage), "T must fit the ring");
+  static constexpr int kCols = NA * RC;                    // adapter rows: TMEM columns
+  static constexpr uint32_t kX = BT * 256, kA = RC * 256;  // 128 k of bf16: two 64-wide boxes
+  static constexpr uint32_t kStage = kX + NA * kA;
+  // an MMA reads 128 token rows from either box of x: past a smaller tile's, and
+  // past the ring's end with the last stage's
+  static constexpr int kSlack = BT < kLanes ? kLanes * 128 : 0;
+  static constexpr int kFit = (192 * 1024 - kSlack) / static_cast<int>(kStage);
+  static constexpr int kStages = kFit < 12 ? kFit : 12;
+  static_assert(BT * (kCols + kPartPad) * 4 <= kStages * static_cast<int>(kStage), "T must fit the ring");
 };
 
-template <int BT, int NA>
+template <int BT, int RC, int NA>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_down_kernel(const __grid_constant__ DownMaps tm, const DownParams p) {
-  using C = Down<BT, NA>;
+  using C = Down<BT, RC, NA>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -64,11 +68,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tok0 = blockIdx.x * BT;
+  const int tok0 = blockIdx.x * BT, j0 = blockIdx.y * C::kCols;
+  const bool quantises = blockIdx.y == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 9);   // the MMAs' commit and eight warps
+      mbar_init(smem_u32(&empty[s]), quantises ? 9 : 1);   // the MMAs' commit, eight warps
     }
     mbar_init(smem_u32(&accum), 1);
     abort_flag = 0;
@@ -110,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_2d(sa + h * (C::kX / 2), &tm.x, kb * 128 + 64 * h, tok0, fb);
 #pragma unroll
         for (int n = 0; n < NA; ++n)
-          tma_load_2d(sa + C::kX + n * kABytes + h * (kABytes / 2), &tm.a, kb * 128 + 64 * h, n * kRows, fb);
+          tma_load_2d(sa + C::kX + n * C::kA + h * (C::kA / 2), &tm.a, kb * 128 + 64 * h, j0 + n * RC, fb);
       }
       if (++s == S) {
         s = 0;
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t idesc = idesc_f32acc(kRows, BT, false);
+    const uint32_t idesc = idesc_f32acc(kLanes, RC, false);
     int s = 0;
     uint32_t ph = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
@@ -134,10 +139,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint64_t xd = sdesc_k_sw128(sa + h * (C::kX / 2));
-          const uint64_t ad = sdesc_k_sw128(sa + C::kX + n * kABytes + h * (kABytes / 2));
+          const uint64_t ad = sdesc_k_sw128(sa + C::kX + n * C::kA + h * (C::kA / 2));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss<false>(tmem + static_cast<uint32_t>(n * BT), ad + 2 * kk, xd + 2 * kk, idesc,
+            mma_ss<false>(tmem + static_cast<uint32_t>(n * RC), xd + 2 * kk, ad + 2 * kk, idesc,
                           (kb > kb0 || h > 0 || kk > 0) ? 1u : 0u);
         }
       mma_commit(smem_u32(&empty[s]));
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
+    for (int kb = kb0; quantises && kb < kb1; ++kb) {
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), ph));
       if (!ok) break;
       const uint8_t* xs = smem + s * C::kStage;
@@ -216,25 +221,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) fail();
     tc_fence_after();
     named_sync(1, 256);   // every warp has read its last tile
-    if (ok) {
-      const int quarter = warp & 3, half = (warp - 2) >> 2;
-      float* stage = reinterpret_cast<float*>(smem);
+    const int quarter = warp & 3, half = (warp - 2) >> 2, token = quarter * 32 + lane;
+    if (ok && quarter * 32 < BT) {
+      float* stage = reinterpret_cast<float*>(smem) + token * (C::kCols + kPartPad);
+      for (int c = half * 16; c < C::kCols; c += 32) {
+        float v[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c), v);
+        if (token < BT) {
 #pragma unroll
-      for (int n = 0; n < NA; ++n)
-        for (int c = half * 16; c < BT; c += 32) {
-          float v[16];
-          tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(n * BT + c), v);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            stage[(n * BT + c + e) * (kRows + kPartPad) + quarter * 32 + lane] = v[e];
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(stage + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
+      }
     }
   }
 
   if (p.splits > 1) cluster_sync_converged();
   else cta_sync_converged();
   if (!abort_flag) {
-    constexpr int kGroups = NA * BT * (kRows / 4);
+    constexpr int kQuads = C::kCols / 4, kGroups = BT * kQuads;
     const int Sp = p.splits;
     const int chunk = (kGroups + Sp - 1) / Sp;
     const int e0 = static_cast<int>(cluster_ctarank()) * chunk, e1 = min(kGroups, e0 + chunk);
@@ -243,10 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int r = 0; r < 8; ++r) peer[r] = map_shared_rank(part0, r < Sp ? r : 0);
     for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += kThreads) {
-      const int row = e / (kRows / 4), j4 = e % (kRows / 4) * 4;
-      const int m = tok0 + row % BT, j = row / BT * kRows + j4;
+      const int token = e / kQuads, j4 = e % kQuads * 4;
+      const int m = tok0 + token, j = j0 + j4;
       if (m >= p.M || j >= p.r) continue;
-      const uint32_t off = static_cast<uint32_t>((row * (kRows + kPartPad) + j4) * 4);
+      const uint32_t off = static_cast<uint32_t>((token * (C::kCols + kPartPad) + j4) * 4);
       float4 v[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -273,19 +278,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BT, int NA>
-uno_status down_launch(const DownMaps& tm, DownParams p, cudaStream_t s) {
-  using C = Down<BT, NA>;
-  const int tiles = (p.M + BT - 1) / BT;
-  int splits = std::max(1, std::min({8, device_sm_count() / tiles, p.nkb}));
+template <int BT, int RC, int NA>
+uno_status down_launch(const Fp8Down& d, DownParams p, cudaStream_t s) {
+  using C = Down<BT, RC, NA>;
+  DownMaps tm;
+  uno_status st;
+  if ((st = make_map(&tm.x, UNO_BF16, d.x, d.K, d.M, d.K, BT)) != UNO_OK) return st;
+  if ((st = make_map(&tm.a, UNO_BF16, d.A, d.K, d.r, d.K, RC)) != UNO_OK) return st;
+  const int tiles = (p.M + BT - 1) / BT, chunks = (p.r + C::kCols - 1) / C::kCols;
+  int splits = std::max(1, std::min({8, device_sm_count() / (tiles * chunks), p.nkb}));
   p.kb_per_split = (p.nkb + splits - 1) / splits;
   p.splits = splits = (p.nkb + p.kb_per_split - 1) / p.kb_per_split;
-  const int smem = static_cast<int>(C::kStages * C::kStage + 1024);
-  auto fn = &fp8_down_kernel<BT, NA>;
+  const int smem = static_cast<int>(C::kStages * C::kStage + C::kSlack + 1024);
+  auto fn = &fp8_down_kernel<BT, RC, NA>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(8-bit down-projection smem)");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(tiles, 1, splits);
+  cfg.gridDim = dim3(tiles, chunks, splits);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -294,11 +303,6 @@ uno_status down_launch(const DownMaps& tm, DownParams p, cudaStream_t s) {
   cfg.attrs = attr;
   e = cudaLaunchKernelEx(&cfg, fn, tm, p);
   return e == cudaSuccess ? UNO_OK : cuda_error(e, "8-bit down-projection launch");
-}
-
-template <int BT>
-uno_status down_dispatch(const DownMaps& tm, const DownParams& p, cudaStream_t s) {
-  return p.r <= kRows ? down_launch<BT, 1>(tm, p, s) : down_launch<BT, 2>(tm, p, s);
 }
 
 }  // namespace
@@ -315,17 +319,13 @@ uno_status fp8_down_launch(const Fp8Down& d, cudaStream_t s) {
   p.xq = d.xq;
   p.sx = d.sx;
   p.t = static_cast<__nv_bfloat16*>(d.t);
-  const int bt = d.M <= 16 ? 16 : d.M <= 32 ? 32 : d.M <= 64 ? 64 : 128;
-  DownMaps tm;
-  uno_status st;
-  if ((st = make_map(&tm.x, UNO_BF16, d.x, d.K, d.M, d.K, bt)) != UNO_OK) return st;
-  if ((st = make_map(&tm.a, UNO_BF16, d.A, d.K, d.r, d.K, kRows)) != UNO_OK) return st;
-  switch (bt) {
-    case 16: return down_dispatch<16>(tm, p, s);
-    case 32: return down_dispatch<32>(tm, p, s);
-    case 64: return down_dispatch<64>(tm, p, s);
-    default: return down_dispatch<128>(tm, p, s);
-  }
+  if (d.M <= 16) return down_launch<16, 32, 1>(d, p, s);
+  if (d.M <= 32) return down_launch<32, 32, 1>(d, p, s);
+  if (d.M <= 64) return down_launch<64, 32, 1>(d, p, s);
+  // chunks of 32 adapter rows while they and eight K-splits leave no SM twice busy
+  const int64_t tiles = (d.M + 127) / 128;
+  if (tiles * ((d.r + 31) / 32) * 8 <= device_sm_count()) return down_launch<128, 32, 1>(d, p, s);
+  return d.r <= 128 ? down_launch<128, 128, 1>(d, p, s) : down_launch<128, 128, 2>(d, p, s);
 }
 
 }  // namespace uno
