@@ -15,6 +15,7 @@
 // HBM bounds it for many rows (3 bytes an element; two separate passes over x
 // measured 43 + 25 us at 4352 x 12288), latency for few.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -278,6 +279,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Clusters of `size` CTAs (along z) of a kernel that a device holds at once.
+template <int BT, int RC, int NA>
+int resident_clusters(int size) {
+  static std::atomic<int> cache[9];
+  if (const int known = cache[size].load(std::memory_order_relaxed)) return known;
+  using C = Down<BT, RC, NA>;
+  const int n = resident_clusters_of(reinterpret_cast<const void*>(&fp8_down_kernel<BT, RC, NA>), kThreads,
+                                     static_cast<int>(C::kStages * C::kStage + C::kSlack + 1024), size);
+  cache[size].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 template <int BT, int RC, int NA>
 uno_status down_launch(const Fp8Down& d, DownParams p, cudaStream_t s) {
   using C = Down<BT, RC, NA>;
@@ -286,7 +299,10 @@ uno_status down_launch(const Fp8Down& d, DownParams p, cudaStream_t s) {
   if ((st = make_map(&tm.x, UNO_BF16, d.x, d.K, d.M, d.K, BT)) != UNO_OK) return st;
   if ((st = make_map(&tm.a, UNO_BF16, d.A, d.K, d.r, d.K, RC)) != UNO_OK) return st;
   const int tiles = (p.M + BT - 1) / BT, chunks = (p.r + C::kCols - 1) / C::kCols;
-  int splits = std::max(1, std::min({8, device_sm_count() / (tiles * chunks), p.nkb}));
+  // as many K-splits as one wave of clusters takes (34 token tiles in four
+  // splits fit the SMs but not the clusters' places: 64 us where three take 39)
+  int splits = std::min(8, p.nkb);
+  while (splits > 1 && static_cast<int64_t>(tiles) * chunks > resident_clusters<BT, RC, NA>(splits)) --splits;
   p.kb_per_split = (p.nkb + splits - 1) / splits;
   p.splits = splits = (p.nkb + p.kb_per_split - 1) / p.kb_per_split;
   const int smem = static_cast<int>(C::kStages * C::kStage + C::kSlack + 1024);
@@ -322,7 +338,7 @@ uno_status fp8_down_launch(const Fp8Down& d, cudaStream_t s) {
   if (d.M <= 16) return down_launch<16, 32, 1>(d, p, s);
   if (d.M <= 32) return down_launch<32, 32, 1>(d, p, s);
   if (d.M <= 64) return down_launch<64, 32, 1>(d, p, s);
-  // chunks of 32 adapter rows while they and eight K-splits leave no SM twice busy
+  // chunks of 32 adapter rows while they and eight K-splits fit the device
   const int64_t tiles = (d.M + 127) / 128;
   if (tiles * ((d.r + 31) / 32) * 8 <= device_sm_count()) return down_launch<128, 32, 1>(d, p, s);
   return d.r <= 128 ? down_launch<128, 128, 1>(d, p, s) : down_launch<128, 128, 2>(d, p, s);

@@ -398,24 +398,8 @@ static_assert(kRows * (kMaxWidth + kPartPad) * 4 <= kRing, "the sums of a split 
 int resident_clusters(int size) {
   static std::atomic<int> cache[9];
   if (const int known = cache[size].load(std::memory_order_relaxed)) return known;
-  int n = 0;
-  auto fn = &fp8_gemm_kernel<false, kMaxWidth>;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(1, 1, size);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kRing + 1024;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = size;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    n = std::max(1, device_sm_count() / size);
-  }
+  const int n = resident_clusters_of(reinterpret_cast<const void*>(&fp8_gemm_kernel<false, kMaxWidth>), kThreads,
+                                     kRing + 1024, size);
   cache[size].store(n, std::memory_order_relaxed);
   return n;
 }
@@ -488,6 +472,27 @@ uno_status gemm_launch(const Fp8Maps& tm, Fp8Params p, cudaStream_t s) {
 }
 
 }  // namespace
+
+int resident_clusters_of(const void* kernel, int threads, int smem, int size) {
+  int n = 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1, 1, size);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = size;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = std::max(1, device_sm_count() / size);
+  }
+  return n;
+}
 
 uno_status fp8_gemm_launch(const Fp8Gemm& g, cudaStream_t s) {
   Fp8Params p{};

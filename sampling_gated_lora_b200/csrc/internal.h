@@ -339,6 +339,8 @@ uno_status wait_selftest_launch(int32_t which, uint64_t limit_ns, int32_t* resul
                                 int32_t* status, cudaStream_t s);
 
 int device_sm_count();
+// Clusters of `size` CTAs along z that the current device holds at once (fp8_gemm.cu).
+int resident_clusters_of(const void* kernel, int threads, int smem, int size);
 // Address of the library-wide status word on the current device (NULL and an
 // error set when it cannot be had).
 int32_t* device_status_word();
