@@ -18,6 +18,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Two bf16 magnitudes, and the larger of two pairs of them (NaN when either is).
+__device__ __forceinline__ uint32_t abs_bf16x2(uint32_t a) { return a & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // 8 floats -> 8 e4m3 codes (nearest even, finite overflow saturates, NaN stays NaN).
 __device__ __forceinline__ uint2 e4m3x8(const float (&f)[8]) {
   uint32_t h[4];

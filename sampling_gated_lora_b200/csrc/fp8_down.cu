@@ -174,13 +174,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = part * kCh + (kCh == 8 ? i ^ (4 * part) : i);   // of the row's 16 chunks
         w[i] = *reinterpret_cast<const uint4*>(xs + (c >> 3) * (C::kX / 2) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
       }
-      float a = kAmaxFloor;
+      uint32_t top[4] = {};   // pairs of magnitudes
 #pragma unroll
       for (int i = 0; i < kCh; ++i) {
         const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a = max_nan(max_nan(a, fabsf(bf16_lo(u[e]))), fabsf(bf16_hi(u[e])));
+        for (int e = 0; e < 4; ++e) top[e] = max_nan_bf16x2(top[e], abs_bf16x2(u[e]));
       }
+      top[0] = max_nan_bf16x2(max_nan_bf16x2(top[0], top[1]), max_nan_bf16x2(top[2], top[3]));
+      float a = max_nan(max_nan(kAmaxFloor, bf16_lo(top[0])), bf16_hi(top[0]));
       // the tile has been read
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[s]));

@@ -59,8 +59,12 @@ struct Vec8<float> {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ float amax8(const Vec8<T>& v) {
+__device__ __forceinline__ float amax8(const Vec8<__nv_bfloat16>& v) {
+  const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(abs_bf16x2(v.w.x), abs_bf16x2(v.w.y)),
+                                    max_nan_bf16x2(abs_bf16x2(v.w.z), abs_bf16x2(v.w.w)));
+  return max_nan(bf16_lo(m), bf16_hi(m));
+}
+__device__ __forceinline__ float amax8(const Vec8<float>& v) {
   float f[8];
   v.get(f);
   float m = fabsf(f[0]);
