@@ -35,6 +35,21 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&f)[8]) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
+// One lane of a converged warp. tcgen05.mma and TMA copies take their operands from
+// uniform registers: issued by a whole warp under elect.sync, from values the
+// compiler knows to be uniform, they cost a few cycles each; issued by a branch
+// `lane == 0` every operand is moved there first (a K-block's four MMAs and commit:
+// 790 -> 330 cycles of the issuing warp, its copies 830 -> 520).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(ok));
+  return ok != 0;
+}
+// The warp's index in its block, known to be uniform.
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+}
+
 // Instruction descriptor of tcgen05.mma kind::f8f6f4, both operands e4m3 and
 // K-major, fp32 accumulator: as idesc_f32acc, with A/B format E4M3 (0).
 __host__ __device__ __forceinline__ uint32_t idesc_e4m3(int m, int n) {

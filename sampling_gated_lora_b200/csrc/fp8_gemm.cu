@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0;
   const int S = kPair ? kPairStages : p.stages;
   const uint32_t x_bytes = kPair ? kRows * 128 : p.x_bytes, stage_bytes = kPair ? 2 * kRows * 128 : p.stage_bytes;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------------------------------------------------- TMA producer
       auto load = [&](uint32_t dst, const CUtensorMap* map, int c, int r, int s) {
         if (kPair) tma_load_2d_pair(dst, map, c, r, map_shared_rank(smem_u32(&full[s]), 0));
@@ -185,63 +185,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       // weights (constant) of the first stages before waiting for the writer of xq and t
       Ring st;
       int skip = min(S, kb1 - kb0);   // blocks of the first tile that are on their way
-      for (int q = 0; q < skip; ++q) {
-        expect(q);
-        load_w(first, kb0 + q, q);
-      }
+      if (elect_one())
+        for (int q = 0; q < skip; ++q) {
+          expect(q);
+          load_w(first, kb0 + q, q);
+        }
+      __syncwarp();
       pdl_wait();
-      for (int q = 0; q < skip; ++q, st.next(S)) load_x(first, kb0 + q, q);
+      for (int q = 0; q < skip; ++q, st.next(S)) {
+        if (elect_one()) load_x(first, kb0 + q, q);
+        __syncwarp();
+      }
       bool ok = true;
       for (int tile = first; ok && tile < p.tiles; tile += step, skip = 0)
         for (int kb = kb0 + skip; kb < kb1; ++kb, st.next(S)) {
-          if (!mbar_wait(smem_u32(&done[st.i]), st.ph ^ 1u) || abort_flag) {
-            fail();
-            ok = false;
-            break;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&done[st.i]), st.ph ^ 1u) && !abort_flag);
+          if (!ok) break;
+          if (elect_one()) {
+            expect(st.i);
+            load_w(tile, kb, st.i);
+            load_x(tile, kb, st.i);
           }
-          expect(st.i);
-          load_w(tile, kb, st.i);
-          load_x(tile, kb, st.i);
+          __syncwarp();
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+      if (!ok && lane == 0) fail();
+    } else if (warp == 1 && rank == 0) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t id8 = idesc_e4m3(kTileRows, kWidth), id16 = idesc_f32acc(kTileRows, kWidth, false);
       Ring st, buf;
       bool ok = true;
       for (int tile = first; ok && tile < p.tiles; tile += step)
         for (int kb = kb0; kb < kb1; ++kb, st.next(S), buf.next(2)) {
-          if (!(kPair ? mbar_wait_cluster(smem_u32(&acce[buf.i]), buf.ph ^ 1u)
-                      : mbar_wait(smem_u32(&acce[buf.i]), buf.ph ^ 1u)) ||
-              !mbar_wait(smem_u32(&full[st.i]), st.ph)) {
-            fail();
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, (kPair ? mbar_wait_cluster(smem_u32(&acce[buf.i]), buf.ph ^ 1u)
+                                              : mbar_wait(smem_u32(&acce[buf.i]), buf.ph ^ 1u)) &&
+                                           mbar_wait(smem_u32(&full[st.i]), st.ph));
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + static_cast<uint32_t>(buf.i * kMaxWidth);
           const uint32_t sa = smem_u32(smem + st.i * stage_bytes);
           const uint64_t xd = sdesc_k_sw128(sa), wd = sdesc_k_sw128(sa + x_bytes);
-          if (kb < p.nkb) {
+          if (elect_one()) {
+            if (kb < p.nkb) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kPair) mma_pair_f8(d, xd + 2 * kk, wd + 2 * kk, id8, kk > 0 ? 1u : 0u);
-              else mma_f8(d, xd + 2 * kk, wd + 2 * kk, id8, kk > 0 ? 1u : 0u);
-            }
-          } else {
+              for (int kk = 0; kk < 4; ++kk) {
+                if (kPair) mma_pair_f8(d, xd + 2 * kk, wd + 2 * kk, id8, kk > 0 ? 1u : 0u);
+                else mma_f8(d, xd + 2 * kk, wd + 2 * kk, id8, kk > 0 ? 1u : 0u);
+              }
+            } else {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kPair) mma_pair_bf16(d, xd + 2 * kk, wd + 2 * kk, id16, kk > 0 ? 1u : 0u);
-              else mma_ss<false>(d, xd + 2 * kk, wd + 2 * kk, id16, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk) {
+                if (kPair) mma_pair_bf16(d, xd + 2 * kk, wd + 2 * kk, id16, kk > 0 ? 1u : 0u);
+                else mma_ss<false>(d, xd + 2 * kk, wd + 2 * kk, id16, kk > 0 ? 1u : 0u);
+              }
             }
+            if (kPair) mma_commit_both(smem_u32(&done[st.i]));
+            else mma_commit(smem_u32(&done[st.i]));
           }
-          if (kPair) mma_commit_both(smem_u32(&done[st.i]));
-          else mma_commit(smem_u32(&done[st.i]));
+          __syncwarp();
         }
+      if (!ok && lane == 0) fail();
     }
   } else {
     // ------------------------------------------------------------ block sums -> registers
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    // (from threadIdx: with the shuffled index the accumulators spill)
+    const int quarter = (threadIdx.x >> 5) & 3, half = (static_cast<int>(threadIdx.x >> 5) - 4) >> 2;
     constexpr int kCols = kWidth / 2;        // of this warp
     constexpr bool kOneScale = kCols % 128 == 0 || 128 % kCols == 0;   // they share one scale of W
     const uint32_t tcol = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kCols);
@@ -405,12 +413,13 @@ int resident_clusters(int size) {
 }
 
 // The launch form with the least estimated time. A K-block of a tile of w
-// features takes about 350 + 1.2 w ns (measured between 128 and 256 features:
-// the chain from an MMA to its buffer's return, the MMA and the adds), and not
-// less than the 2.8 w ns in which HBM brings its w rows of W to one SM of 148
-// when W passes by once. CTA pairs take the same time for twice the tokens, less
-// 3 % (equal to 7 % faster at 2048 .. 8192 rows); single CTAs fill the device
-// with half the tokens a tile, and can split K.
+// features takes about 380 + 0.63 w ns (measured between 128 and 256 features at
+// 2048 x 12288 -> 4096: an epilogue warp's wait, loads and adds), and not less
+// than the 2.8 w ns in which HBM brings its w rows of W to one SM of 148 when W
+// passes by once. CTA pairs take 2 % longer for twice the tokens (544 .. 4352
+// rows); up to 256 rows they read W once where two token tiles that drift apart
+// read it twice (136 x 4096 -> 151936: 197 us against 221). Single CTAs fill the
+// device with half the tokens a tile, and can split K.
 struct Plan {
   bool pair;
   int width;
@@ -426,9 +435,9 @@ Plan plan(Fp8Params* p) {
     const int64_t tiles = static_cast<int64_t>(tiles_m) * ((p->N + w - 1) / w);
     if (splits > 1 && tiles > resident_clusters(splits)) return false;   // one wave of clusters only
     const int per = (nkb + splits - 1) / splits;
-    double block = 350. + 1.2 * w;
-    if (tiles_m == 1) block = std::max(block, 2.8 * w);
-    if (pair) block *= 0.97;
+    double block = 380. + 0.63 * w;
+    if (tiles_m == 1) block = std::max(block, pair ? 1.4 * w : 2.8 * w);
+    if (pair) block *= p->M <= 2 * kRows ? 0.97 : 1.02;
     const double cost = static_cast<double>((tiles + slots - 1) / slots) * per * block;
     if (least < 0. || cost < least) {
       least = cost;
