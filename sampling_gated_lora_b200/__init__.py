@@ -238,6 +238,39 @@ def _expect(t, shape, dtypes, name, optional=False):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
 
 
+def _operands(*specs):
+    """Index of the CUDA device of a call's tensors, after the checks of _expect and _dev in one pass
+    (a decode call is short: they were a third of its host time). specs: (tensor, shape or None for
+    any, dtype, name, optional)."""
+    device, apart = None, False
+    for t, shape, dtype, name, optional in specs:
+        if t is None:
+            if not optional:
+                raise ValueError(f"{name} is required")
+            continue
+        if shape is not None and (t.shape != shape or t.dtype is not dtype):
+            _expect(t, shape, (dtype,), name)
+        d = t.get_device()
+        if device is None:
+            device = d
+        if d != device or d < 0 or not t.is_contiguous():
+            apart = True
+    if apart:
+        _dev(*(spec[0] for spec in specs))
+    return device
+
+
+def _launch_on(device, stream, cfn, *args):
+    """_launch for a device index."""
+    cuda = _torch()._C
+    if stream is not None or device != cuda._cuda_getDevice():
+        _launch(_torch().device("cuda", device), stream, cfn, *args)
+        return
+    st = cfn(*args, cuda._cuda_getCurrentRawStream(device))
+    if st:
+        _check(st)
+
+
 def _floats():
     torch = _torch()
     return (torch.bfloat16, torch.float32)
@@ -260,9 +293,9 @@ def _allocating_on(stream):
 
 
 def _new(like, shape, dtype, stream):
-    """An uninitialised tensor on like's device for work on `stream`."""
+    """An uninitialised tensor on like's device for work on `stream` (dtype None: like's)."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     with _allocating_on(stream):
         return like.new_empty(shape, dtype=dtype)
 
@@ -372,21 +405,20 @@ def fp8_quantize(x, block_rows=1, codes=None, scales=None, stream=None):
     """(codes [M,K] float8_e4m3fn, scales [ceil(M/block_rows), ceil(K/128)] float32) of x [M,K]
     (bf16 or f32) in blocks of block_rows (1 or 128) x 128: scale = max |x| / 448."""
     torch = _torch()
-    _expect(x, (None, None), _floats(), "x")
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+        _expect(x, (None, None), _floats(), "x")
     M, K = x.shape
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    f8, f32 = torch.float8_e4m3fn, torch.float32
     shape = (M if block_rows == 1 else _blocks(M), _blocks(K))
-    _expect(codes, (M, K), (torch.float8_e4m3fn,), "codes", optional=True)
-    _expect(scales, shape, (torch.float32,), "scales", optional=True)
-    L = load()
-    dev = _dev(x, codes, scales)
+    dev = _operands((x, None, None, "x", False), (codes, (M, K), f8, "codes", True), (scales, shape, f32, "scales", True))
     if codes is None:
-        codes = _new(x, (M, K), torch.float8_e4m3fn, stream)
+        codes = _new(x, (M, K), f8, stream)
     if scales is None:
-        scales = _new(x, shape, torch.float32, stream)
-    _launch(dev, stream, L.uno_fp8_quantize, _dtype(x), M, K, block_rows, _ptr(x), _ptr(codes),
-            _ptr(scales))
+        scales = _new(x, shape, f32, stream)
+    _launch_on(dev, stream, load().uno_fp8_quantize, _dtype(x), M, K, block_rows, x.data_ptr(), codes.data_ptr(),
+               scales.data_ptr())
     return codes, scales
 
 
@@ -401,26 +433,7 @@ def gated_lora_linear_fp8(x, Wq, Ws, A, Bl, gate, scale=1.0, y=None, workspace=N
     Ws [ceil(N/128), ceil(K/128)] float32 (fp8_quantize(W, 128)); x is quantised per row and block of
     128 for the product with W, the adapter reads it as it is. bf16 x, A, Bl and y; A = Bl = None: no
     adapter."""
-    torch = _torch()
-    bf16, f8, f32 = (torch.bfloat16,), (torch.float8_e4m3fn,), (torch.float32,)
-    _expect(x, (None, None), bf16, "x")
-    M, K = x.shape
-    _expect(Wq, (None, K), f8, "Wq")
-    N = Wq.shape[0]
-    _expect(Ws, (_blocks(N), _blocks(K)), f32, "Ws")
-    r = A.shape[0] if A is not None else 0
-    _expect(A, (r, K), bf16, "A", optional=r == 0)
-    _expect(Bl, (N, r), bf16, "Bl", optional=r == 0)
-    _expect(gate, (M,), (torch.uint8,), "gate", optional=r == 0)
-    _expect(y, (M, N), bf16, "y", optional=True)
-    L = load()
-    dev = _dev(x, Wq, Ws, A, Bl, gate, y, workspace)
-    if y is None:
-        y = _new(x, (M, N), x.dtype, stream)
-    ws, wsb = _workspace(gated_lora_linear_fp8_workspace(M, K, N, r), dev, workspace, stream)
-    _launch(dev, stream, L.uno_gated_lora_linear_fp8, UNO_BF16, M, K, N, r, _ptr(x), _ptr(Wq),
-            _ptr(Ws), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(y), _ptr(ws), wsb)
-    return y
+    return _linear_fp8(x, Wq, Ws, A, Bl, gate, scale, y, workspace, stream, False)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -435,26 +448,43 @@ def gated_lora_input_grad_fp8(dy, Wqt, Wst, A, Bl, gate, scale=1.0, dx=None, wor
     [M,N] bf16. The weight comes transposed, laid out once: Wqt = Wq.t().contiguous() [K,N],
     Wst = Ws.t().contiguous(); A [r,K] and Bl [N,r] as in the forward pass. dy is quantised per row
     and block of 128 along N for the product with W."""
+    return _linear_fp8(dy, Wqt, Wst, A, Bl, gate, scale, dx, workspace, stream, True)
+
+
+def _linear_fp8(x, Wq, Ws, A, Bl, gate, scale, y, workspace, stream, grad):
+    """The two calls above: the weight is [y's width, x's width] in both."""
     torch = _torch()
-    bf16, f8, f32 = (torch.bfloat16,), (torch.float8_e4m3fn,), (torch.float32,)
-    _expect(dy, (None, None), bf16, "dy")
-    M, N = dy.shape
-    _expect(Wqt, (None, N), f8, "Wqt")
-    K = Wqt.shape[0]
-    _expect(Wst, (_blocks(K), _blocks(N)), f32, "Wst")
+    bf16, f8, f32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32
+    nx, nw, ns, ny = ("dy", "Wqt", "Wst", "dx") if grad else ("x", "Wq", "Ws", "y")
+    if x.dim() != 2 or x.dtype is not bf16:
+        _expect(x, (None, None), (bf16,), nx)
+    M, kx = x.shape
+    if Wq.dim() != 2:
+        _expect(Wq, (None, kx), (f8,), nw)
+    ky = Wq.shape[0]
+    K, N = (ky, kx) if grad else (kx, ky)
     r = A.shape[0] if A is not None else 0
-    _expect(A, (r, K), bf16, "A", optional=r == 0)
-    _expect(Bl, (N, r), bf16, "Bl", optional=r == 0)
-    _expect(gate, (M,), (torch.uint8,), "gate", optional=r == 0)
-    _expect(dx, (M, K), bf16, "dx", optional=True)
+    dev = _operands((x, None, None, nx, False), (Wq, (ky, kx), f8, nw, False),
+                    (Ws, ((ky + 127) // 128, (kx + 127) // 128), f32, ns, False), (A, (r, K), bf16, "A", r == 0),
+                    (Bl, (N, r), bf16, "Bl", r == 0), (gate, (M,), torch.uint8, "gate", r == 0),
+                    (y, (M, ky), bf16, ny, True), (workspace, None, None, "workspace", True))
     L = load()
-    dev = _dev(dy, Wqt, Wst, A, Bl, gate, dx, workspace)
-    if dx is None:
-        dx = _new(dy, (M, K), dy.dtype, stream)
-    ws, wsb = _workspace(gated_lora_input_grad_fp8_workspace(M, K, N, r), dev, workspace, stream)
-    _launch(dev, stream, L.uno_gated_lora_input_grad_fp8, UNO_BF16, M, K, N, r, _ptr(dy), _ptr(Wqt),
-            _ptr(Wst), _ptr(A), _ptr(Bl), _ptr(gate), float(scale), _ptr(dx), _ptr(ws), wsb)
-    return dx
+    if grad:
+        fn, need = L.uno_gated_lora_input_grad_fp8, gated_lora_input_grad_fp8_workspace
+    else:
+        fn, need = L.uno_gated_lora_linear_fp8, gated_lora_linear_fp8_workspace
+    if y is None:
+        y = _new(x, (M, ky), None, stream)
+    if workspace is None:
+        workspace, _ = _workspace(need(M, K, N, r), x.device, None, stream)
+    if r:
+        a, bl, g = A.data_ptr(), Bl.data_ptr(), gate.data_ptr()
+    else:
+        a = bl = g = None
+    _launch_on(dev, stream, fn, UNO_BF16, M, K, N, r, x.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), a, bl, g,
+               float(scale), y.data_ptr(), _ptr(workspace),
+               0 if workspace is None else workspace.nbytes)
+    return y
 
 
 def _verify_shapes(p_logits, q_logits, draft, accepted_len, out_tokens, out_count, dev_status):
@@ -601,18 +631,18 @@ def token_counts_add(counts, tokens, lens=None, slots=None, prompt=False, dev_st
     [S,V] int16, rows slots [B] (default: row b): bit 15 = in the prompt (prompt=True sets it),
     bits 0-14 = times emitted (prompt=False adds one each). Returns counts."""
     torch = _torch()
-    i32 = (torch.int32,)
-    _expect(counts, (None, None), (torch.int16,), "counts")
+    i16, i32 = torch.int16, torch.int32
+    if counts.dim() != 2 or counts.dtype is not i16:
+        _expect(counts, (None, None), (i16,), "counts")
     S, V = counts.shape
-    _expect(tokens, (None, None), i32, "tokens")
+    if tokens.dim() != 2 or tokens.dtype is not i32:
+        _expect(tokens, (None, None), (i32,), "tokens")
     B, T = tokens.shape
-    _expect(lens, (B,), i32, "lens", optional=True)
-    _expect(slots, (B,), i32, "slots", optional=True)
-    _expect(dev_status, (1,), i32, "dev_status", optional=True)
-    L = load()
-    dev = _dev(counts, tokens, lens, slots, dev_status)
-    _launch(dev, stream, L.uno_token_counts_add, S, V, _ptr(counts), B, T, _ptr(tokens), _ptr(lens),
-            _ptr(slots), 1 if prompt else 0, _ptr(dev_status))
+    dev = _operands((counts, None, None, "counts", False), (tokens, None, None, "tokens", False),
+                    (lens, (B,), i32, "lens", True), (slots, (B,), i32, "slots", True),
+                    (dev_status, (1,), i32, "dev_status", True))
+    _launch_on(dev, stream, load().uno_token_counts_add, S, V, counts.data_ptr(), B, T, tokens.data_ptr(), _ptr(lens),
+               _ptr(slots), 1 if prompt else 0, _ptr(dev_status))
     return counts
 
 
@@ -627,33 +657,28 @@ def logits_process(logits, out=None, counts=None, slots=None, draft=None, repeti
     float32; mask [B,R,ceil(V/32)] int32 words, bit v % 32 of word v // 32 set: id v allowed, else -inf.
     """
     torch = _torch()
-    i32, f32 = (torch.int32,), (torch.float32,)
-    _expect(logits, (None, None, None), _floats(), "logits")
+    i32, f32 = torch.int32, torch.float32
+    if logits.dim() != 3 or logits.dtype not in (torch.bfloat16, f32):
+        _expect(logits, (None, None, None), _floats(), "logits")
     B, R, V = logits.shape
-    _expect(out, (B, R, V), (logits.dtype,), "out", optional=True)
-    _expect(counts, (None, V), (torch.int16,), "counts", optional=True)
-    _expect(slots, (B,), i32, "slots", optional=True)
-    per_row = draft is not None and draft.dim() == 3
-    _expect(draft, (B, R, None) if per_row else (B, None), i32, "draft", optional=True)
-    _expect(repetition, (B,), f32, "repetition", optional=True)
-    _expect(frequency, (B,), f32, "frequency", optional=True)
-    _expect(presence, (B,), f32, "presence", optional=True)
-    _expect(bias_ids, (B, None), i32, "bias_ids", optional=bias is None)
-    nb = 0 if bias_ids is None else bias_ids.shape[1]
-    _expect(bias, (B, nb), f32, "bias", optional=bias_ids is None)
-    _expect(mask, (B, R, (V + 31) // 32), i32, "mask", optional=True)
-    _expect(dev_status, (1,), i32, "dev_status", optional=True)
-    L = load()
-    dev = _dev(logits, out, counts, slots, draft, repetition, frequency, presence, bias_ids, bias,
-               mask, dev_status)
+    S = 0 if counts is None or counts.dim() != 2 else counts.shape[0]
+    per_row, P = False, 0
+    if draft is not None:
+        per_row = draft.dim() == 3
+        P = draft.shape[-1] if draft.dim() else 0
+    nb = 0 if bias_ids is None or bias_ids.dim() != 2 else bias_ids.shape[1]
+    dev = _operands((logits, None, None, "logits", False), (out, (B, R, V), logits.dtype, "out", True),
+                    (counts, (S, V), torch.int16, "counts", True), (slots, (B,), i32, "slots", True),
+                    (draft, (B, R, P) if per_row else (B, P), i32, "draft", True),
+                    (repetition, (B,), f32, "repetition", True), (frequency, (B,), f32, "frequency", True),
+                    (presence, (B,), f32, "presence", True), (bias_ids, (B, nb), i32, "bias_ids", bias is None),
+                    (bias, (B, nb), f32, "bias", bias_ids is None), (mask, (B, R, (V + 31) // 32), i32, "mask", True),
+                    (dev_status, (1,), i32, "dev_status", True))
     if out is None:
-        with _allocating_on(stream):
-            out = torch.empty_like(logits)
-    _launch(dev, stream, L.uno_logits_process, _dtype(logits), B, R, V, _ptr(logits), _ptr(out),
-            0 if counts is None else counts.shape[0], _ptr(counts), _ptr(slots),
-            0 if draft is None else draft.shape[-1], 1 if per_row else 0, _ptr(draft),
-            _ptr(repetition), _ptr(frequency), _ptr(presence), nb, _ptr(bias_ids), _ptr(bias),
-            _ptr(mask), _ptr(dev_status))
+        out = _new(logits, (B, R, V), None, stream)
+    _launch_on(dev, stream, load().uno_logits_process, _dtype(logits), B, R, V, logits.data_ptr(), out.data_ptr(), S,
+               _ptr(counts), _ptr(slots), P, 1 if per_row else 0, _ptr(draft), _ptr(repetition), _ptr(frequency),
+               _ptr(presence), nb, _ptr(bias_ids), _ptr(bias), _ptr(mask), _ptr(dev_status))
     return out
 
 

@@ -309,7 +309,8 @@ uno_status down_launch(const Fp8Down& d, DownParams p, cudaStream_t s) {
   p.splits = splits = (p.nkb + p.kb_per_split - 1) / p.kb_per_split;
   const int smem = static_cast<int>(C::kStages * C::kStage + C::kSlack + 1024);
   auto fn = &fp8_down_kernel<BT, RC, NA>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemGranted granted;
+  cudaError_t e = granted.ask(reinterpret_cast<const void*>(fn), smem);
   if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(8-bit down-projection smem)");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles, chunks, splits);

@@ -464,7 +464,8 @@ uno_status gemm_launch(const Fp8Maps& tm, Fp8Params p, cudaStream_t s) {
   p.stages = std::min(12, static_cast<int>((kRing - past) / p.stage_bytes));
   const int smem = kRing + 1024;
   auto fn = &fp8_gemm_kernel<kPair, kWidth>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemGranted granted;
+  cudaError_t e = granted.ask(reinterpret_cast<const void*>(fn), smem);
   if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(8-bit GEMM smem)");
   const int slots = kPair ? std::max(1, device_sm_count() / 2) : device_sm_count();
   const int ctas = p.splits > 1 ? p.tiles : std::min(p.tiles, slots);

@@ -1,6 +1,7 @@
 // Host-side declarations shared by the C-ABI layer and the kernel files.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <utility>
@@ -339,6 +340,20 @@ uno_status wait_selftest_launch(int32_t which, uint64_t limit_ns, int32_t* resul
                                 int32_t* status, cudaStream_t s);
 
 int device_sm_count();
+// Dynamic shared memory of one kernel, asked for once per device.
+struct SmemGranted {
+  std::atomic<uint64_t> devices{0};
+  cudaError_t ask(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (e == cudaSuccess && !(devices.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_release);
+    }
+    return e;
+  }
+};
 // Clusters of `size` CTAs along z that the current device holds at once (fp8_gemm.cu).
 int resident_clusters_of(const void* kernel, int threads, int smem, int size);
 // Address of the library-wide status word on the current device (NULL and an
