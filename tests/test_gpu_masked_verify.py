@@ -5,7 +5,7 @@ import pytest
 
 import workloads as W
 from oracle import sampling as S
-from gpu_util import check_verify_outputs_valid, compare_verify, dev_tensor
+from gpu_util import check_verify_outputs_valid, compare_drafts, compare_verify, dev_tensor
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,15 @@ def test_a_row_without_a_finite_logit_and_a_nan_among_masked_ones_are_reported()
     acc, tok, cnt = U.psi_verify(_enc(p, "f32"), _enc(q, "f32"), dev_tensor(d, "i32"), 1.0, 9, 4)
     assert U.device_status() & U.DEV_NAN
     assert int(acc[1]) == -1 and int(acc[2]) == -1 and int(acc[0]) >= 0 and (tok[1:] == -1).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,allowed", [(1000, 3), (1001, 1), (20000, 5), (151936, 12), (151936, 140000)])
+def test_draft_on_masked_rows(V, allowed, dtype):
+    import sampling_gated_lora_b200 as U
+    B, k = 6, 3
+    _, q, _, on = _masked(B, k, k + 1, V, allowed, dtype, seed=V + allowed)
+    d = U.draft_sample(_enc(q, dtype), 1.0, 9, 4).cpu().numpy()
+    _, bad = compare_drafts(d, q, 1.0, 9, 4)
+    assert not bad and U.device_status() == 0
+    assert on[np.arange(B)[:, None], d].all()
