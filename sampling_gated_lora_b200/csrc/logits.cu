@@ -14,8 +14,10 @@
 //   z' = -inf                                   if the row's mask bit is 0
 // computed in float and rounded once to the logits' type.
 //
-// HBM bandwidth bounds both: every logit is read and written once, the record
-// and the mask once. Few ids have a record, a bias or a place on the path, so
+// Every logit is read and written once, the record and the mask once. At 256 x 9
+// rows of 151936 (275 us) that is 0.85 of the copy rate, but instruction issue is
+// the nearer bound (ALU pipe 0.67 busy; a denser mask or none takes the same
+// time), so what follows counts instructions. Few ids have a record, a bias or a place on the path, so
 // the dense pass only branches per 16-byte vector on "any record here", and
 // the ids of the path and the bias list (at most a few hundred) are recomputed
 // from the original logits by single threads and overwrite the dense result.
@@ -105,18 +107,30 @@ struct LogitVec<__nv_bfloat16> {
                                                    apply_rules(r, bf16_hi(z), c >> 16));
     return *reinterpret_cast<const uint32_t*>(&h);   // an id without a record comes back as it was
   }
-  static __device__ __forceinline__ void rules(uint4& z, const uint4& c, const Rules& r) {
-    if (c.x) z.x = two(z.x, c.x, r);
-    if (c.y) z.y = two(z.y, c.y, r);
-    if (c.z) z.z = two(z.z, c.z, r);
-    if (c.w) z.w = two(z.w, c.w, r);
+  // the first pair with a record each round: a warp whose lanes hold one such
+  // pair each, wherever in the vector, takes one round instead of up to four
+  static __device__ __forceinline__ void rules(uint4& z, uint4 c, const Rules& r) {
+    while (c.x | c.y | c.z | c.w) {
+      const bool p0 = c.x != 0u, p1 = !p0 && c.y != 0u, p2 = !p0 && !p1 && c.z != 0u, p3 = !p0 && !p1 && !p2;
+      const uint32_t v = two(p0 ? z.x : p1 ? z.y : p2 ? z.z : z.w, p0 ? c.x : p1 ? c.y : p2 ? c.z : c.w, r);
+      if (p0) z.x = v, c.x = 0u;
+      if (p1) z.y = v, c.y = 0u;
+      if (p2) z.z = v, c.z = 0u;
+      if (p3) z.w = v, c.w = 0u;
+    }
   }
-  static __device__ __forceinline__ uint32_t forbid2(uint32_t z, uint32_t bits) {   // two ids, two bits
-    const uint32_t keep = (bits & 1u ? 0xffffu : 0u) | (bits & 2u ? 0xffff0000u : 0u);
+  // keep two ids by the sign bits of two bytes of w
+  template <uint32_t kSelect>
+  static __device__ __forceinline__ uint32_t forbid2(uint32_t z, uint32_t w) {
+    uint32_t keep;   // prmt with bit 3 of a selector: eight copies of the byte's sign
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(keep) : "r"(w), "n"(kSelect));
     return (z & keep) | (0xff80ff80u & ~keep);
   }
   static __device__ __forceinline__ void forbid(uint4& z, uint32_t bits) {
-    z = make_uint4(forbid2(z.x, bits), forbid2(z.y, bits >> 2), forbid2(z.z, bits >> 4), forbid2(z.w, bits >> 6));
+    // four bits to the signs of four bytes: bit i times 2^(7 (i + 1)) is bit 8 i + 7,
+    // and the four products do not meet
+    const uint32_t lo = (bits & 15u) * 0x10204080u, hi = (bits >> 4) * 0x10204080u;
+    z = make_uint4(forbid2<0x9988>(z.x, lo), forbid2<0xbbaa>(z.y, lo), forbid2<0x9988>(z.z, hi), forbid2<0xbbaa>(z.w, hi));
   }
 };
 template <>
@@ -292,7 +306,9 @@ __global__ void __launch_bounds__(kThreads + 32, kAligned ? kCtas : kCtas - 1)
     constexpr uint32_t kAll = (1u << kN) - 1u;
     if (kAligned) {
       if (v >= V) return 0u;
-      return mask ? (reinterpret_cast<const uint8_t*>(mask)[v >> 3] >> (v & 7)) & kAll : kAll;
+      if (!mask) return kAll;
+      const uint32_t byte = reinterpret_cast<const uint8_t*>(mask)[static_cast<uint32_t>(v) >> 3];
+      return kN == 8 ? byte : (byte >> (v & 7)) & kAll;
     }
     uint32_t bits = 0u;
 #pragma unroll
@@ -344,7 +360,7 @@ __global__ void __launch_bounds__(kThreads + 32, kAligned ? kCtas : kCtas - 1)
           Vec::rules(z[u], make_uint4(w[0], w[1], w[2], w[3]), r);
         }
         if (now[u] != (1u << kN) - 1u) Vec::forbid(z[u], now[u]);
-        __stcs(reinterpret_cast<uint4*>(out + v), z[u]);
+        *reinterpret_cast<uint4*>(out + v) = z[u];
       } else if (!kAligned) {
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
