@@ -294,10 +294,12 @@ def _allocating_on(stream):
 
 def _new(like, shape, dtype, stream):
     """An uninitialised tensor on like's device for work on `stream` (dtype None: like's)."""
-    if stream is None:
-        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
-    with _allocating_on(stream):
-        return like.new_empty(shape, dtype=dtype)
+    if stream is not None:
+        with _allocating_on(stream):
+            return _new(like, shape, dtype, None)
+    if like.shape == shape:   # the quickest of torch's ways for each case
+        return _torch().empty_like(like) if dtype is None else _torch().empty_like(like, dtype=dtype)
+    return like.new_empty(*shape) if dtype is None else like.new_empty(*shape, dtype=dtype)
 
 
 # ---------------------------------------------------------------- operations
