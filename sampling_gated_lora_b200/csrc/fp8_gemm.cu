@@ -16,8 +16,8 @@
 //
 // Few tokens: HBM bandwidth bounds it (9 x 4096 -> 151936: 622 MB of codes in
 // 129 us, 0.74 of the copy rate). Many: an epilogue warp's wait, TMEM loads and
-// adds of a K-block, about 1000 cycles where the tensor core needs 512
-// (2048 x 12288 -> 4096: 130 us with the down-projection; 4352 rows: 266).
+// adds of a K-block, about 860 cycles where the tensor core needs 512
+// (2048 x 12288 -> 4096: 111 us, 130 with the down-projection; 4352 rows: 266).
 #include <algorithm>
 #include <atomic>
 
@@ -96,18 +96,17 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
 //
 // kPair (cta_group::2, many tokens): CTA r holds tokens [128 r, 128 r + 128) of
 // the A side and half of the tile's W rows; each CTA loads 32 KB a K-block for
-// what a CTA alone would load 48 KB for.
-// Otherwise (few tokens; HBM bandwidth bounds it) one CTA computes the tile;
-// x comes in only as many rows as there are, epilogue warps without tokens only
+// what a CTA alone would load 48 KB for, and W passes once for 256 tokens.
+// Otherwise one CTA computes the tile; x comes in only as many rows as there are, epilogue warps without tokens only
 // pass the buffers on, and with fewer tiles than SMs K is split over a
 // thread-block cluster whose sums meet through distributed shared memory in
 // rank order.
 //
 // Threads: warp 0 TMA producer, warp 1 MMA issuer (kPair: the leader's), both
 // converged (elect_one), warps 2 and 3 idle, warps 4..11 epilogue (sixteen with
-// half the columns each: 141 us where these take 131, 2048 x 12288 -> 4096). The launch gives every thread 168
-// registers; the first warpgroup hands all but 56 of its own to the two
-// epilogue warpgroups, whose 128 sums a thread need more
+// half the columns each: 141 us where these take 131, 2048 x 12288 -> 4096).
+// The launch gives every thread 168 registers; the first warpgroup hands all but
+// 56 of its own to the two epilogue warpgroups, whose 128 sums a thread need more
 // (128 (56 + 2 * 224) = 384 * 168).
 template <bool kPair, int kWidth>
 __global__ void __launch_bounds__(kThreads, 1)
