@@ -223,8 +223,10 @@ uno_status uno_gated_lora_input_grad_fp8(uno_dtype dt, int64_t M, int64_t K, int
  *       if n = k and k_p = k+1: the bonus, same rule on p_k with u3;
  *     padded with -1; out_count[b] = number of tokens written.
  *   out_tokens is [B, k+1]. T > 0. 1 <= k <= 32, 2 <= V <= 196608. Logits of
- *   -inf have probability 0 (masked ids); a row of nothing but -inf is reported
- *   like one with a NaN.
+ *   -inf have probability 0 (masked ids). A NaN in a row of the k drafted
+ *   positions, or in the bonus row when n = k, sets UNO_DEV_NAN and that
+ *   sequence's outputs are -1; a row of nothing but -inf is reported like one
+ *   with a NaN.
  *   dev_status: optional int32 device word, OR-ed with UNO_DEV_* bits.
  * ------------------------------------------------------------------------- */
 size_t uno_psi_verify_workspace(int32_t B, int32_t k, int32_t k_p, int32_t V);

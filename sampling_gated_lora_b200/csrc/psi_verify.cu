@@ -842,6 +842,12 @@ __global__ void __launch_bounds__(kDrawThreads, 4)
       s_n = rej ? __ffs(rej) - 1 : k;
       s_bad = badm != 0;
       s_nan = nanm != 0;
+      if (!rej && a.k_p == k + 1) {   // the bonus row is read only when every draft is accepted
+        const float2 sp = row_stat(a.stats, b * a.k_p + k, a.chunks, a.c);
+        s_stat[0] = sp.x;
+        s_stat[1] = sp.y;
+        if (isnan(sp.y)) s_nan = 1;
+      }
     }
   }
   cta_sync();
@@ -876,15 +882,13 @@ __global__ void __launch_bounds__(kDrawThreads, 4)
   // Rows of the draw: residual at position n (p row and q row), or the bonus p row k.
   const int prow = b * a.k_p + (residual ? n : k);
   const int qrow_local = b * k + n;   // q row index within q_logits
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && residual) {   // (the bonus row's are there)
     const float2 sp = row_stat(a.stats, prow, a.chunks, a.c);
+    const float2 sq = row_stat(a.stats, rows_p + qrow_local, a.chunks, a.c);
     s_stat[0] = sp.x;
     s_stat[1] = sp.y;
-    if (residual) {
-      const float2 sq = row_stat(a.stats, rows_p + qrow_local, a.chunks, a.c);
-      s_stat[2] = sq.x;
-      s_stat[3] = sq.y;
-    }
+    s_stat[2] = sq.x;
+    s_stat[3] = sq.y;
   }
   int lo, len;
   chunk_range(V, static_cast<int>(nrank), static_cast<int>(rank), &lo, &len);
@@ -1812,18 +1816,20 @@ __global__ void __launch_bounds__(32) vp_decide_kernel(const VpParams a) {
   const uint32_t badm = __ballot_sync(0xffffffffu, bad) & in_k;
   const uint32_t nanm = __ballot_sync(0xffffffffu, nan) & in_k;
   const int n = rej ? __ffs(rej) - 1 : k;
+  const int pos = n < k ? n : (a.k_p == k + 1 ? k : -1);
+  // the bonus row is read only when every draft is accepted
+  const bool nans = nanm || (pos == k && isnan(vp_merge(a.parts_p, rows_p, b * a.k_p + k, a.G, a.c).y));
   int32_t* tok = a.out_tokens + static_cast<size_t>(b) * (k + 1);
-  if (badm || nanm) {
+  if (badm || nans) {
     if (j == 0) {
       a.accepted_len[b] = -1;
       a.out_count[b] = -1;
       a.draw[b] = -1;
-      raise_status(a.status, (badm ? kDevBadDraft : 0) | (nanm ? kDevNaN : 0));
+      raise_status(a.status, (badm ? kDevBadDraft : 0) | (nans ? kDevNaN : 0));
     }
     for (int i = j; i <= k; i += 32) tok[i] = -1;
     return;
   }
-  const int pos = n < k ? n : (a.k_p == k + 1 ? k : -1);
   for (int i = j; i <= k; i += 32) tok[i] = i < n ? a.draft[b * k + i] : -1;
   if (j == 0) {
     a.accepted_len[b] = n;
