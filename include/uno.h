@@ -214,7 +214,8 @@ uno_status uno_gated_lora_input_grad_fp8(uno_dtype dt, int64_t M, int64_t K, int
  *   and uniforms u from Philox4x32-10 (counter = (b_global*k + j, step lo,
  *   step hi, stream), key = (seed lo, seed hi), u = (word0 >> 8) * 2^-24,
  *   b_global = seq_offset + b; stream 1 accept, 2 residual, 3 bonus):
- *     accept position j iff u1 * q_j(d_j) < p_j(d_j);
+ *     accept position j iff u1 * q_j(d_j) < p_j(d_j) (an id with p = 0 is
+ *     never accepted, one with q = 0 < p always);
  *     n = first rejected position (k if none)          -> accepted_len[b]
  *     out_tokens[b] = d_0..d_{n-1}, then
  *       if n < k: r = smallest v with C(v) > u2 * C(V-1), C the inclusive

@@ -80,10 +80,11 @@ def cdf_margin(weights, u, v):
 def accept_threshold(p_d, q_d):
     """The u-threshold of the accept test: d is accepted iff u < min(1, p(d)/q(d)).
 
-    q(d) = 0 cannot occur for a draft drawn from q; it is treated as accept.
+    q(d) = 0 cannot occur for a draft drawn from q. The test u q(d) < p(d) decides it: accept
+    where p(d) > 0, reject an id that p gives nothing (masked).
     """
     if q_d == 0:
-        return 1
+        return 1 if p_d > 0 else 0
     ratio = p_d / q_d
     return 1 if ratio >= 1 else ratio
 
@@ -120,7 +121,7 @@ def verify_sequence(p_logits, q_logits, draft, T: float, seed: int, step: int, b
     """Verify one sequence's block. p_logits [k_p,V], q_logits [k,V], draft [k].
 
     Returns a dict with accepted_len n, the emitted tokens, and diagnostics:
-      u_accept[j], ratio[j] = p_j(d_j)/q_j(d_j) (inf if q = 0),
+      u_accept[j], ratio[j] = p_j(d_j)/q_j(d_j) (if q = 0: inf, or 0 where p = 0 too),
       draw ("residual", "residual_p", "bonus" or None), u_draw, draw_margin
       (distance of the draw's threshold to the nearest CDF edge of the chosen
       token, relative to the total weight).
@@ -139,7 +140,7 @@ def verify_sequence(p_logits, q_logits, draft, T: float, seed: int, step: int, b
     for j in range(k):
         d = int(draft[j])
         pd, qd = p[j, d], q[j, d]
-        ratio[j] = pd / qd if qd > 0 else np.inf
+        ratio[j] = pd / qd if qd > 0 else (np.inf if pd > 0 else 0.0)
         if n == k and not (u1[j] < accept_threshold(pd, qd)):
             n = j
     tokens = [int(t) for t in draft[:n]]

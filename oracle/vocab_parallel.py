@@ -52,7 +52,7 @@ def row_partials(z, ids, v0, T):
     for i in range(R):
         m = z[i].max() if Vs else -np.inf
         out[i, 0] = m
-        out[i, 1] = np.exp(z[i] - m).sum() if Vs else 0.0
+        out[i, 1] = np.exp(z[i] - m).sum() if m > -np.inf else 0.0   # (a shard may be masked whole)
         d = int(ids[i]) - v0 if ids is not None else -1
         out[i, 2] = z[i, d] if 0 <= d < Vs else -np.inf
     return out
@@ -88,7 +88,7 @@ def verify_decide(p_parts, q_parts, draft, k, k_p, seed, step, seq_offset):
         for j in range(k):
             pr, qr = b * k_p + j, b * k + j
             pd, qd = _prob(zp[pr], Mp[pr], Sp[pr]), _prob(zq[qr], Mq[qr], Sq[qr])
-            if not (qd == 0 or u1[j] * qd < pd):
+            if not u1[j] * qd < pd:
                 n = j
                 break
         kind = "residual" if n < k else ("bonus" if k_p == k + 1 else None)

@@ -122,6 +122,23 @@ __device__ __forceinline__ void merge_stat(float& m, float& s, float m2, float s
   m = mx;
 }
 
+// The accept test u q(d) < p(d) with p(d) = 2^ep / sp, q(d) = 2^eq / sq. Where
+// both have left float's range it is taken on their logarithms: an id masked in
+// the AR row (ep = -inf) is rejected, one that both rows hold very unlikely is not
+// mistaken for it.
+__device__ __forceinline__ bool accepts(float u, float ep, float sp, float eq, float sq) {
+  const float pd = fast_exp2(ep) / sp, qd = fast_exp2(eq) / sq;
+  if (pd == 0.f && qd == 0.f) return log2f(u) + (eq - log2f(sq)) < ep - log2f(sp);
+  return u * qd < pd;
+}
+
+// max(p - q, 0) of one id, p = wp / Sp and q = wq / Sq each rounded first (as one
+// fused operation it would be rounding noise instead of 0 where the rows are equal,
+// and a draw after a masked draft would follow the noise instead of p).
+__device__ __forceinline__ float residual_of(float wp, float inv_sp, float wq, float inv_sq) {
+  return fmaxf(__fsub_rn(__fmul_rn(wp, inv_sp), __fmul_rn(wq, inv_sq)), 0.f);
+}
+
 // (max, sum of 2^((z - max) c)) of ids [lo, hi) of row z over the CTA
 // (kStatThreads threads, every one calls): 16-byte loads, four in flight per
 // thread, each thread an online stat, then shuffle and shared-memory merges.
@@ -827,11 +844,9 @@ __global__ void __launch_bounds__(kDrawThreads, 4)
       if (!bad && !nan) {
         const float zp = to_f32<T>(p_logits[static_cast<size_t>(prow) * V + d]);
         const float zq = to_f32<T>(q_logits[static_cast<size_t>(b * k + j) * V + d]);
-        const float pd = fast_exp2((zp - sp.x) * a.c) / sp.y;
-        const float qd = fast_exp2((zq - sq.x) * a.c) / sq.y;
         const uint32_t idx = static_cast<uint32_t>(bg * static_cast<uint64_t>(k) + j);
         const float u1 = uniform24(philox_word0(a.seed, a.step, kStreamAccept, idx));
-        acc = (qd == 0.f) || (u1 * qd < pd);
+        acc = accepts(u1, (zp - sp.x) * a.c, sp.y, (zq - sq.x) * a.c, sq.y);
       }
     }
     const uint32_t in_k = k >= 32 ? 0xffffffffu : ((1u << k) - 1u);
@@ -927,7 +942,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4)
           load8_bf16(gq, i, len, zw);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            w[j] = fmaxf(fast_exp2((zv[j] - Mp) * c) * inv_sp - fast_exp2((zw[j] - Mq) * c) * inv_sq, 0.f);
+            w[j] = residual_of(fast_exp2((zv[j] - Mp) * c), inv_sp, fast_exp2((zw[j] - Mq) * c), inv_sq);
         };
         token = cluster_draw8(sh, w8_res, lo, len, u, &zero);
       } else {
@@ -940,9 +955,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4)
   }
   if (residual) {
     auto w_res = [&](int i) {
-      const float p = fast_exp2((to_f32<T>(zp[i]) - Mp) * c) * inv_sp;
-      const float q = fast_exp2((to_f32<T>(zq[i]) - Mq) * c) * inv_sq;
-      return fmaxf(p - q, 0.f);
+      return residual_of(fast_exp2((to_f32<T>(zp[i]) - Mp) * c), inv_sp, fast_exp2((to_f32<T>(zq[i]) - Mq) * c), inv_sq);
     };
     token = cluster_draw(sh, w_res, lo, len, u, &zero);
   } else {
@@ -1142,14 +1155,17 @@ __global__ void __launch_bounds__(kDrawThreads)
       if (!((live >> i) & 1u)) continue;
       if (threadIdx.x == 0) {
         const int x = cand[i * k + j];
-        const float px = fast_exp2((to_f32<T>(prow[x]) - Mp) * c) * inv_sp;
-        const float qx = fast_exp2((to_f32<T>(qrow[x]) - Mq) * c) * inv_sq;
-        const float r = static_cast<float>(tree_target(px, qx, s_Zinv, nz));
         const uint32_t idx = static_cast<uint32_t>(
             (bg * static_cast<uint64_t>(k) + static_cast<uint64_t>(j)) * static_cast<uint64_t>(N) +
             static_cast<uint64_t>(i));
         const float u1 = uniform24(philox_word0(a.seed, a.step, kStreamAccept, idx));
-        s_flag[0] = (qx == 0.f) || (u1 * qx < r);
+        const float ep = (to_f32<T>(prow[x]) - Mp) * c, eq = (to_f32<T>(qrow[x]) - Mq) * c;
+        if (nz == 0) {
+          s_flag[0] = accepts(u1, ep, s_stat[1], eq, s_stat[3]);
+        } else {
+          const float qx = fast_exp2(eq) * inv_sq;
+          s_flag[0] = u1 * qx < static_cast<float>(tree_target(fast_exp2(ep) * inv_sp, qx, s_Zinv, nz));
+        }
       }
       cta_sync();
       const bool acc = s_flag[0] != 0;
@@ -1804,11 +1820,9 @@ __global__ void __launch_bounds__(32) vp_decide_kernel(const VpParams a) {
     const float3 sq = vp_merge(a.parts_q, rows_q, b * k + j, a.G, a.c);
     nan = isnan(sp.y) || isnan(sq.y);
     if (!bad && !nan) {
-      const float pd = sp.z > -INFINITY ? fast_exp2((sp.z - sp.x) * a.c) / sp.y : 0.f;
-      const float qd = sq.z > -INFINITY ? fast_exp2((sq.z - sq.x) * a.c) / sq.y : 0.f;
       const uint32_t idx = static_cast<uint32_t>(bg * static_cast<uint64_t>(k) + j);
       const float u1 = uniform24(philox_word0(a.seed, a.step, kStreamAccept, idx));
-      acc = (qd == 0.f) || (u1 * qd < pd);
+      acc = accepts(u1, (sp.z - sp.x) * a.c, sp.y, (sq.z - sq.x) * a.c, sq.y);
     }
   }
   const uint32_t in_k = k >= 32 ? 0xffffffffu : ((1u << k) - 1u);
@@ -1874,10 +1888,10 @@ __global__ void __launch_bounds__(kDrawThreads)
   const float inv_sp = 1.f / st.y, inv_sq = residual ? 1.f / st.w : 0.f;
   double r = 0.0, pm = 0.0;
   for (int v = threadIdx.x; v < a.Vs; v += blockDim.x) {
-    const float pv = fast_exp2((to_f32<T>(pr[v]) - st.x) * a.c) * inv_sp;
-    const float qv = residual ? fast_exp2((to_f32<T>(qr[v]) - st.z) * a.c) * inv_sq : 0.f;
-    r += static_cast<double>(fmaxf(pv - qv, 0.f));
-    pm += static_cast<double>(pv);
+    const float wp = fast_exp2((to_f32<T>(pr[v]) - st.x) * a.c);
+    const float wq = residual ? fast_exp2((to_f32<T>(qr[v]) - st.z) * a.c) : 0.f;
+    r += static_cast<double>(residual_of(wp, inv_sp, wq, inv_sq));
+    pm += static_cast<double>(wp * inv_sp);
   }
   r = block_sum(r, slots);
   pm = block_sum(pm, slots);
@@ -1946,9 +1960,7 @@ __global__ void __launch_bounds__(kDrawThreads)
   int v;
   if (s_res) {
     auto w_res = [&](int i) {
-      const float pv = fast_exp2((to_f32<T>(pr[i]) - st.x) * c) * inv_sp;
-      const float qv = fast_exp2((to_f32<T>(qr[i]) - st.z) * c) * inv_sq;
-      return fmaxf(pv - qv, 0.f);
+      return residual_of(fast_exp2((to_f32<T>(pr[i]) - st.x) * c), inv_sp, fast_exp2((to_f32<T>(qr[i]) - st.z) * c), inv_sq);
     };
     v = block_draw(sh, w_res, a.Vs, s_tl);
   } else {
