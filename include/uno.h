@@ -53,7 +53,7 @@ typedef enum { UNO_BF16 = 0, UNO_F32 = 1 } uno_dtype;
 
 /* Device status bits (dev_status words and uno_device_status). */
 #define UNO_DEV_BAD_DRAFT 1 /* a draft id outside [0, V): that sequence's outputs are -1 */
-#define UNO_DEV_NAN 2       /* a NaN logit (or no finite one) in a row that was read: outputs are -1 */
+#define UNO_DEV_NAN 2       /* a NaN logit in a row that was read, or no finite one in a row needed: outputs -1 */
 #define UNO_DEV_TIMEOUT 4   /* a bounded on-device wait gave up (kernel returned early) */
 #define UNO_DEV_BAD_INDEX 8 /* a token id or a slot outside its range: that entry was skipped */
 #define UNO_DEV_NO_TOKEN 16 /* a logits row whose mask allows no token: its logits are all -inf */
@@ -226,8 +226,9 @@ uno_status uno_gated_lora_input_grad_fp8(uno_dtype dt, int64_t M, int64_t K, int
  *   out_tokens is [B, k+1]. T > 0. 1 <= k <= 32, 2 <= V <= 196608. Logits of
  *   -inf have probability 0 (masked ids). A NaN in a row of the k drafted
  *   positions, or in the bonus row when n = k, sets UNO_DEV_NAN and that
- *   sequence's outputs are -1; a row of nothing but -inf is reported like one
- *   with a NaN.
+ *   sequence's outputs are -1. A row of nothing but -inf is reported the same
+ *   way where the outputs depend on it: up to position n, or as the bonus row.
+ *   Behind the first rejection such rows are fine.
  *   dev_status: optional int32 device word, OR-ed with UNO_DEV_* bits.
  * ------------------------------------------------------------------------- */
 size_t uno_psi_verify_workspace(int32_t B, int32_t k, int32_t k_p, int32_t V);
@@ -298,8 +299,8 @@ uno_status uno_psi_verify_noalloc(uno_dtype dt, int32_t B, int32_t k, int32_t k_
  *   Sizes: 1 <= N <= 32, 1 <= k <= 32, 1 <= R <= N*k + 1, V as for
  *   uno_psi_verify; B * (R + k) <= 2^30; (seq_offset + B) * (k + 1) * N <= 2^32.
  *   Device-detected: a candidate token outside [0, V), more trie nodes than
- *   R (UNO_DEV_BAD_DRAFT) or a NaN logit in a row the walk reads
- *   (UNO_DEV_NAN) set the status bits; that sequence's outputs are -1.
+ *   R (UNO_DEV_BAD_DRAFT) or a row that the walk reads and that holds a NaN
+ *   or no finite logit (UNO_DEV_NAN) set the status bits; that sequence's outputs are -1.
  *   workspace: >= uno_tree_verify_workspace(B, N, k, R, V) bytes, 16-byte
  *   aligned, any contents.
  * ------------------------------------------------------------------------- */

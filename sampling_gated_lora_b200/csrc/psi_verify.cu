@@ -132,6 +132,13 @@ __device__ __forceinline__ bool accepts(float u, float ep, float sp, float eq, f
   return u * qd < pd;
 }
 
+// Whether one of the positions without a finite logit lies before the first
+// rejected one (bit masks): those behind it are never asked for, and a draft that
+// has left a grammar leaves such rows behind.
+__device__ __forceinline__ bool empty_needed(uint32_t empty, uint32_t rejected) {
+  return empty && (!rejected || __ffs(empty) < __ffs(rejected));
+}
+
 // max(p - q, 0) of one id, p = wp / Sp and q = wq / Sq each rounded first (as one
 // fused operation it would be rounding noise instead of 0 where the rows are equal,
 // and a draw after a masked draft would follow the noise instead of p).
@@ -494,8 +501,8 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
   }
 }
 
-// Merge the chunk stats of one row. A row without a finite logit has no
-// distribution: its sum is NaN, as with a NaN logit.
+// Merge the chunk stats of one row. A row without a distribution has no positive
+// sum: NaN with a NaN logit, 0 without a finite one.
 __device__ __forceinline__ float2 row_stat(const float2* stats, int row, int chunks, float c) {
   float m = -INFINITY, s = 0.f;
   bool nan = false;
@@ -504,7 +511,7 @@ __device__ __forceinline__ float2 row_stat(const float2* stats, int row, int chu
     nan |= isnan(v.y);
     merge_stat(m, s, v.x, v.y, c);
   }
-  return make_float2(m, nan || m == -INFINITY ? NAN : s);
+  return make_float2(m, nan ? NAN : s);
 }
 
 // ------------------------------------------------------------------ cluster inverse-CDF draw
@@ -833,7 +840,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4)
 
   if (threadIdx.x < 32) {
     const int j = threadIdx.x;
-    bool acc = true, bad = false, nan = false;
+    bool acc = true, bad = false, nan = false, empty = false;
     if (j < k) {
       const int d = a.draft[b * k + j];
       bad = d < 0 || d >= V;
@@ -841,7 +848,8 @@ __global__ void __launch_bounds__(kDrawThreads, 4)
       const float2 sp = row_stat(a.stats, prow, a.chunks, a.c);
       const float2 sq = row_stat(a.stats, qrow, a.chunks, a.c);
       nan = isnan(sp.y) || isnan(sq.y);
-      if (!bad && !nan) {
+      empty = sp.y == 0.f || sq.y == 0.f;
+      if (!bad && !nan && !empty) {
         const float zp = to_f32<T>(p_logits[static_cast<size_t>(prow) * V + d]);
         const float zq = to_f32<T>(q_logits[static_cast<size_t>(b * k + j) * V + d]);
         const uint32_t idx = static_cast<uint32_t>(bg * static_cast<uint64_t>(k) + j);
@@ -853,15 +861,16 @@ __global__ void __launch_bounds__(kDrawThreads, 4)
     const uint32_t rej = __ballot_sync(0xffffffffu, !acc) & in_k;
     const uint32_t badm = __ballot_sync(0xffffffffu, bad) & in_k;
     const uint32_t nanm = __ballot_sync(0xffffffffu, nan) & in_k;
+    const uint32_t emptym = __ballot_sync(0xffffffffu, empty) & in_k;
     if (j == 0) {
       s_n = rej ? __ffs(rej) - 1 : k;
       s_bad = badm != 0;
-      s_nan = nanm != 0;
+      s_nan = nanm || empty_needed(emptym, rej);
       if (!rej && a.k_p == k + 1) {   // the bonus row is read only when every draft is accepted
         const float2 sp = row_stat(a.stats, b * a.k_p + k, a.chunks, a.c);
         s_stat[0] = sp.x;
         s_stat[1] = sp.y;
-        if (isnan(sp.y)) s_nan = 1;
+        if (!(sp.y > 0.f)) s_nan = 1;
       }
     }
   }
@@ -1138,7 +1147,7 @@ __global__ void __launch_bounds__(kDrawThreads)
       s_stat[1] = sp.y;
       s_stat[2] = sq.x;
       s_stat[3] = sq.y;
-      s_flag[3] = isnan(sp.y) || isnan(sq.y);
+      s_flag[3] = !(sp.y > 0.f && sq.y > 0.f);
     }
     cta_sync();
     if (s_flag[3]) {
@@ -1246,7 +1255,7 @@ __global__ void __launch_bounds__(kDrawThreads)
   if (threadIdx.x == 0) {
     const float2 sp = row_stat(a.stats, b * R + node, a.chunks, c);
     s_stat[0] = sp.x;
-    s_flag[3] = isnan(sp.y);
+    s_flag[3] = !(sp.y > 0.f);
   }
   cta_sync();
   if (s_flag[3]) {
@@ -1802,7 +1811,7 @@ __device__ __forceinline__ float3 vp_merge(const float4* parts, int rows, int ro
     merge_stat(m, s, v.x, v.y, c);
     z = fmaxf(z, v.z);
   }
-  return make_float3(m, nan || m == -INFINITY ? NAN : s, z);   // as row_stat
+  return make_float3(m, nan ? NAN : s, z);   // as row_stat
 }
 
 // One warp per sequence: lane j tests position j (as verify_finalize).
@@ -1812,14 +1821,15 @@ __global__ void __launch_bounds__(32) vp_decide_kernel(const VpParams a) {
   const int b = blockIdx.x, j = threadIdx.x, k = a.k;
   const int rows_p = a.B * a.k_p, rows_q = a.B * k;
   const uint64_t bg = a.seq_offset + static_cast<uint64_t>(b);
-  bool acc = true, bad = false, nan = false;
+  bool acc = true, bad = false, nan = false, empty = false;
   if (j < k) {
     const int d = a.draft[b * k + j];
     bad = d < 0 || d >= a.V;
     const float3 sp = vp_merge(a.parts_p, rows_p, b * a.k_p + j, a.G, a.c);
     const float3 sq = vp_merge(a.parts_q, rows_q, b * k + j, a.G, a.c);
     nan = isnan(sp.y) || isnan(sq.y);
-    if (!bad && !nan) {
+    empty = sp.y == 0.f || sq.y == 0.f;
+    if (!bad && !nan && !empty) {
       const uint32_t idx = static_cast<uint32_t>(bg * static_cast<uint64_t>(k) + j);
       const float u1 = uniform24(philox_word0(a.seed, a.step, kStreamAccept, idx));
       acc = accepts(u1, (sp.z - sp.x) * a.c, sp.y, (sq.z - sq.x) * a.c, sq.y);
@@ -1829,10 +1839,12 @@ __global__ void __launch_bounds__(32) vp_decide_kernel(const VpParams a) {
   const uint32_t rej = __ballot_sync(0xffffffffu, !acc) & in_k;
   const uint32_t badm = __ballot_sync(0xffffffffu, bad) & in_k;
   const uint32_t nanm = __ballot_sync(0xffffffffu, nan) & in_k;
+  const uint32_t emptym = __ballot_sync(0xffffffffu, empty) & in_k;
   const int n = rej ? __ffs(rej) - 1 : k;
   const int pos = n < k ? n : (a.k_p == k + 1 ? k : -1);
   // the bonus row is read only when every draft is accepted
-  const bool nans = nanm || (pos == k && isnan(vp_merge(a.parts_p, rows_p, b * a.k_p + k, a.G, a.c).y));
+  const bool nans = nanm || empty_needed(emptym, rej) ||
+                    (pos == k && !(vp_merge(a.parts_p, rows_p, b * a.k_p + k, a.G, a.c).y > 0.f));
   int32_t* tok = a.out_tokens + static_cast<size_t>(b) * (k + 1);
   if (badm || nans) {
     if (j == 0) {

@@ -85,3 +85,46 @@ def test_a_bonus_row_without_a_distribution_is_reported(form, dtype, V, what):
     assert st == U.DEV_NAN and acc[1] == -1 and cnt[1] == -1 and np.all(tok[1] == -1)
     _, wrong = compare_verify((acc, tok, cnt), want, k, [0, 2, 3])
     assert not wrong
+
+
+@pytest.mark.parametrize("form,dtype,V", FORMS)
+def test_rows_behind_the_first_rejection_may_be_empty(form, dtype, V):
+    """A drafted id leaves the grammar (p = 0 there) and the AR rows behind it, the bonus row among them, allow nothing:
+    the accepted prefix and its replacement token come out as with any other rows there."""
+    B, k = 4, 3
+    p, q, d = _same_rows(B, k, V, seed=V + 1)
+    p[1, 1, d[1, 1]] = -np.inf    # rejected at position 1
+    p[2, 0, d[2, 0]] = -np.inf    # at position 0
+    want = S.psi_verify(p, q, d, 1.0, SEED, STEP)
+    assert want["accepted_len"].tolist() == [k, 1, 0, k]
+    bad = p.copy()
+    bad[1, 2:] = bad[2, 1:] = -np.inf
+    acc, tok, cnt, st = _verify(form, bad, q, d, dtype)
+    assert st == 0
+    _, wrong = compare_verify((acc, tok, cnt), want, k, range(B))
+    assert not wrong
+
+
+@pytest.mark.parametrize("form,dtype,V", FORMS)
+def test_empty_rows_up_to_the_first_rejection_are_reported(form, dtype, V):
+    import sampling_gated_lora_b200 as U
+    B, k = 4, 3
+    p, q, d = _same_rows(B, k, V, seed=V + 2)
+    p[1, 2, d[1, 2]] = -np.inf
+    p[1, 1] = -np.inf             # needed before the rejection at position 2
+    p[2, 0] = -np.inf             # the first row
+    q[3, 1] = -np.inf             # no draft distribution where the block is still accepted
+    acc, tok, cnt, st = _verify(form, p, q, d, dtype)
+    assert st == U.DEV_NAN and np.all(acc[1:] == -1) and np.all(cnt[1:] == -1) and np.all(tok[1:] == -1)
+    assert acc[0] == k
+
+
+@pytest.mark.parametrize("form,dtype,V", [f for f in FORMS if f[0] != "tree"])   # the walk reads no row behind its end
+def test_a_nan_at_any_drafted_position_is_reported(form, dtype, V):
+    import sampling_gated_lora_b200 as U
+    B, k = 2, 3
+    p, q, d = _same_rows(B, k, V, seed=V + 3)
+    p[1, 0, d[1, 0]] = -np.inf
+    p[1, 2, V - 1] = np.nan
+    acc, tok, cnt, st = _verify(form, p, q, d, dtype)
+    assert st == U.DEV_NAN and acc[0] == k and acc[1] == -1 and cnt[1] == -1 and np.all(tok[1] == -1)
