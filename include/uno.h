@@ -433,13 +433,14 @@ uno_status uno_draft_sample(uno_dtype dt, int32_t B, int32_t k, int32_t V, const
  *     z' = z' - frequency[b] n(v) - presence[b] [n(v) > 0]
  *     z' = z' + sum of bias[b,i] over bias_ids[b,i] = v
  *     z' = -inf   where bit v of mask[b,j] is 0 (whatever the logit was)
- *   in float, rounded once to `dt`. Path tokens: path [B,P] (path_per_row 0) is
+ *   in float, rounded once to `dt` (UNO_BF16: z / repetition as the product with
+ *   the float reciprocal). Path tokens: path [B,P] (path_per_row 0) is
  *   the drafted block, of which row j follows the first min(j, P) ids (the k or
  *   k + 1 AR rows of uno_psi_verify); path [B,R,P] (path_per_row 1) gives each
  *   row its own ids (the nodes of uno_tree_verify). -1 entries of path and
  *   bias_ids are skipped, other ids outside [0, V) too with UNO_DEV_BAD_INDEX.
  *   A slot outside [0, S) counts as an empty record and sets that bit.
- *   repetition (> 0), frequency, presence [B] float, NULL: 1, 0, 0. bias_ids
+ *   repetition (>= 2^-126), frequency, presence [B] float, NULL: 1, 0, 0. bias_ids
  *   [B,nb] int32, bias [B,nb] float (nb = 0: none). mask [B,R,ceil(V/32)]
  *   words, bit v % 32 of word v / 32, NULL: all allowed. A row that allows
  *   nothing gets -inf everywhere and sets UNO_DEV_NO_TOKEN.
