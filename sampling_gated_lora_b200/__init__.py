@@ -153,13 +153,15 @@ def _check(st: int):
 # ---------------------------------------------------------------- marshalling helpers
 
 _torch_module = None
+_raw_stream = None   # torch's query of a device's current cudaStream_t, where this torch has it
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _raw_stream
     if _torch_module is None:
         import torch
         _torch_module = torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return _torch_module
 
 
@@ -167,13 +169,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _current_stream(index):
+    """cudaStream_t of torch's current stream on device `index` (the raw query saves building a
+    Stream object)."""
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return _torch().cuda.current_stream(index).cuda_stream
+
+
 def _stream(stream, device=None):
     """cudaStream_t of `stream` (default: the current stream of `device`); an
     explicit stream must belong to `device`."""
     torch = _torch()
     if stream is None:
-        if device is not None and device.index is not None:   # without building a Stream object
-            return torch._C._cuda_getCurrentRawStream(device.index)
+        if device is not None and device.index is not None:
+            return _current_stream(device.index)
         stream = torch.cuda.current_stream(device)
     elif device is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
@@ -262,11 +272,10 @@ def _operands(*specs):
 
 def _launch_on(device, stream, cfn, *args):
     """_launch for a device index."""
-    cuda = _torch()._C
-    if stream is not None or device != cuda._cuda_getDevice():
+    if stream is not None or device != _torch().cuda.current_device():
         _launch(_torch().device("cuda", device), stream, cfn, *args)
         return
-    st = cfn(*args, cuda._cuda_getCurrentRawStream(device))
+    st = cfn(*args, _current_stream(device))
     if st:
         _check(st)
 
