@@ -15,10 +15,10 @@
 // HBM bounds it for many rows (3 bytes an element; two separate passes over x
 // measured 43 + 25 us at 4352 x 12288), latency for few.
 #include <algorithm>
-#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
+#include "per_device.h"
 
 #include "fp8.cuh"
 
@@ -281,16 +281,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Clusters of `size` CTAs (along z) of a kernel that a device holds at once.
+// Clusters of `size` CTAs (along z) of a kernel that `device` (the current one) holds at once.
 template <int BT, int RC, int NA>
-int resident_clusters(int size) {
-  static std::atomic<int> cache[9];
-  if (const int known = cache[size].load(std::memory_order_relaxed)) return known;
+int resident_clusters(int device, int size) {
+  static PerDevice<9> kept;
   using C = Down<BT, RC, NA>;
-  const int n = resident_clusters_of(reinterpret_cast<const void*>(&fp8_down_kernel<BT, RC, NA>), kThreads,
-                                     static_cast<int>(C::kStages * C::kStage + C::kSlack + 1024), size);
-  cache[size].store(n, std::memory_order_relaxed);
-  return n;
+  return kept.get(device, size, [&] {
+    return resident_clusters_of(reinterpret_cast<const void*>(&fp8_down_kernel<BT, RC, NA>), kThreads,
+                                static_cast<int>(C::kStages * C::kStage + C::kSlack + 1024), size);
+  });
 }
 
 template <int BT, int RC, int NA>
@@ -304,7 +303,8 @@ uno_status down_launch(const Fp8Down& d, DownParams p, cudaStream_t s) {
   // as many K-splits as one wave of clusters takes (34 token tiles in four
   // splits fit the SMs but not the clusters' places: 64 us where three take 39)
   int splits = std::min(8, p.nkb);
-  while (splits > 1 && static_cast<int64_t>(tiles) * chunks > resident_clusters<BT, RC, NA>(splits)) --splits;
+  const int device = current_device();
+  while (splits > 1 && static_cast<int64_t>(tiles) * chunks > resident_clusters<BT, RC, NA>(device, splits)) --splits;
   p.kb_per_split = (p.nkb + splits - 1) / splits;
   p.splits = splits = (p.nkb + p.kb_per_split - 1) / p.kb_per_split;
   const int smem = static_cast<int>(C::kStages * C::kStage + C::kSlack + 1024);

@@ -19,10 +19,10 @@
 // adds of a K-block, about 860 cycles where the tensor core needs 512
 // (2048 x 12288 -> 4096: 111 us, 130 with the down-projection; 4352 rows: 266).
 #include <algorithm>
-#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
+#include "per_device.h"
 
 #include "fp8.cuh"
 
@@ -407,14 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kRing = 196 * 1024;   // bytes of the stage ring
 static_assert(kRows * (kMaxWidth + kPartPad) * 4 <= kRing, "the sums of a split tile must fit the ring");
 
-// Clusters of `size` CTAs (along z) that a device holds at once.
-int resident_clusters(int size) {
-  static std::atomic<int> cache[9];
-  if (const int known = cache[size].load(std::memory_order_relaxed)) return known;
-  const int n = resident_clusters_of(reinterpret_cast<const void*>(&fp8_gemm_kernel<false, kMaxWidth>), kThreads,
-                                     kRing + 1024, size);
-  cache[size].store(n, std::memory_order_relaxed);
-  return n;
+// Clusters of `size` CTAs (along z) that `device` (the current one) holds at once.
+int resident_clusters(int device, int size) {
+  static PerDevice<9> kept;
+  return kept.get(device, size, [&] {
+    return resident_clusters_of(reinterpret_cast<const void*>(&fp8_gemm_kernel<false, kMaxWidth>), kThreads,
+                                kRing + 1024, size);
+  });
 }
 
 // The launch form with the least estimated time. A K-block of a tile of w
@@ -431,14 +430,14 @@ struct Plan {
 };
 
 Plan plan(Fp8Params* p) {
-  const int nkb = p->nkb + p->nkr, sms = device_sm_count();
+  const int nkb = p->nkb + p->nkr, sms = device_sm_count(), device = current_device();
   Plan best{};
   double least = -1.;
   auto consider = [&](bool pair, int w, int splits) {
     const int rows = pair ? 2 * kRows : kRows, slots = pair ? std::max(1, sms / 2) : sms;
     const int tiles_m = (p->M + rows - 1) / rows;
     const int64_t tiles = static_cast<int64_t>(tiles_m) * ((p->N + w - 1) / w);
-    if (splits > 1 && tiles > resident_clusters(splits)) return false;   // one wave of clusters only
+    if (splits > 1 && tiles > resident_clusters(device, splits)) return false;   // one wave of clusters only
     const int per = (nkb + splits - 1) / splits;
     double block = 380. + 0.63 * w;
     if (tiles_m == 1) block = std::max(block, pair ? 1.4 * w : 2.8 * w);

@@ -491,6 +491,11 @@ int device_sm_count() {
   return n;
 }
 
+int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 uno_status gemm_prepare(const GemmProblem& pb, GemmLaunch* out) {
   out->sk_flag = nullptr;
   out->sk_flag_bytes = 0;

@@ -340,6 +340,7 @@ uno_status wait_selftest_launch(int32_t which, uint64_t limit_ns, int32_t* resul
                                 int32_t* status, cudaStream_t s);
 
 int device_sm_count();
+int current_device();   // -1: none
 // Dynamic shared memory of one kernel, asked for once per device.
 struct SmemGranted {
   std::atomic<uint64_t> devices{0};
