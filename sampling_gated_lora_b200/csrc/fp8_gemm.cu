@@ -462,10 +462,9 @@ Plan plan(Fp8Params* p) {
 
 template <bool kPair, int kWidth>
 uno_status gemm_launch(const Fp8Maps& tm, Fp8Params p, cudaStream_t s) {
-  // an MMA reads 128 rows of x whatever the stage holds of them; where a stage is
-  // smaller than that, what it reads past the last one stays within the ring
-  const uint32_t past = p.stage_bytes < kRows * 128 ? kRows * 128 - p.stage_bytes : 0;
-  p.stages = std::min(12, static_cast<int>((kRing - past) / p.stage_bytes));
+  // an MMA reads 128 rows of x whatever the stage holds of them: past x it reads W's
+  static_assert(kPair || kWidth >= kRows, "128 rows of a stage that holds any of x must lie within it");
+  p.stages = std::min(12, static_cast<int>(kRing / p.stage_bytes));
   const int smem = kRing + 1024;
   auto fn = &fp8_gemm_kernel<kPair, kWidth>;
   static SmemGranted granted;
