@@ -399,7 +399,8 @@ uno_status uno_vp_draft_draw(uno_dtype dt, int32_t B, int32_t k, int32_t Vs, int
  *   q_logits [B,k,V] `dt`; draft [B,k] int32 (device).
  *   workspace: >= uno_draft_sample_workspace(B, k, V) bytes, 16-byte
  *   aligned, any contents (per-row, per-vocab-chunk softmax statistics).
- *   A row holding a NaN logit gets draft -1 and sets UNO_DEV_NAN.
+ *   A row holding a NaN logit, or no finite one, gets draft -1 and sets
+ *   UNO_DEV_NAN.
  * ------------------------------------------------------------------------- */
 size_t uno_draft_sample_workspace(int32_t B, int32_t k, int32_t V);
 

@@ -17,7 +17,9 @@
 // Few tokens: HBM bandwidth bounds it (9 x 4096 -> 151936: 622 MB of codes in
 // 129 us, 0.74 of the copy rate). Many: an epilogue warp's wait, TMEM loads and
 // adds of a K-block, about 860 cycles where the tensor core needs 512
-// (2048 x 12288 -> 4096: 111 us, 130 with the down-projection; 4352 rows: 266).
+// (2048 x 12288 -> 4096: 111 us, 130 with the down-projection; 4352 rows: 266;
+// single calls after a pause, 150 and 311 in a stream of calls at the clock that the
+// power cap leaves).
 #include <algorithm>
 
 #include "common.cuh"
@@ -253,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ block sums -> registers
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    // (from threadIdx: with the shuffled index the accumulators spill)
+    // (from threadIdx: with the shuffled index the accumulators spill; this way the
+    // pair form still spills five words, the others none)
     const int quarter = (threadIdx.x >> 5) & 3, half = (static_cast<int>(threadIdx.x >> 5) - 4) >> 2;
     constexpr int kCols = kWidth / 2;        // of this warp
     constexpr bool kOneScale = kCols % 128 == 0 || 128 % kCols == 0;   // they share one scale of W
@@ -422,7 +425,8 @@ int resident_clusters(int device, int size) {
 // than the 2.8 w ns in which HBM brings its w rows of W to one SM of 148 when W
 // passes by once. CTA pairs take 2 % longer for twice the tokens (544 .. 4352
 // rows); up to 256 rows they read W once where two token tiles that drift apart
-// read it twice (136 x 4096 -> 151936: 197 us against 221). Single CTAs fill the
+// read it twice (136 x 4096 -> 151936: 197 us against 221; the 0.97 below is from
+// that size alone and stands for every N and K). Single CTAs fill the
 // device with half the tokens a tile, and can split K.
 struct Plan {
   bool pair;

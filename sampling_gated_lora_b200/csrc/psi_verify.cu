@@ -813,7 +813,7 @@ struct FinalizeParams {
 };
 
 // One cluster per sequence; blockDim = kDrawThreads. Four CTAs per SM (64
-// registers a thread: one 4-byte spill) when the draw reads its rows in
+// registers a thread; the float form spills 4 bytes) when the draw reads its rows in
 // place: psi_verify B=256, k=16 470 us against 484 at three CTAs per SM.
 template <typename T>
 __global__ void __launch_bounds__(kDrawThreads, 4)
